@@ -16,6 +16,8 @@ Functions mirror the C entry points:
   kda_decode_step_gated(q, k, v, z, A_log, beta, state, ...)   the same with the input prologue
   kda_decode_spec(prev, n_accepted, cur, state, ...)   speculative verification with state replay
   kda_fwd_workspace_size(...), kda_workspace_status(ws), kda_status_string(s)
+  kda_conv_fwd / kda_conv_step, kda_ssm_fwd / kda_ssm_step, kda_group_norm   (layer.py) the short
+                                                 convolution, the selective scan and the gated group norm
 and ``kda_fwd_host`` runs kda_fwd on host (pinned) tensors through the C
 entry point of the same name, which copies inputs in and outputs back on the
 given stream.
@@ -504,3 +506,7 @@ def kda_fwd_host(q, k, v, log_alpha, beta, init_state=None, cu_seqlens=None, dev
                               dk, dv, ctypes.c_void_p(s.cuda_stream), _DT[q.dtype], _ptr(ws), ws.numel())
     _check(code, "kda_fwd_host")
     return dev_buffers["out_h"], fin_h, dev_buffers
+
+
+from .layer import (KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU, kda_conv_fwd, kda_conv_step,  # noqa: E402,F401
+                    kda_group_norm, kda_ssm_fwd, kda_ssm_fwd_workspace_size, kda_ssm_step)

@@ -1,0 +1,122 @@
+// Shared pieces of the operators around a recurrent layer (short convolution,
+// selective scan, group norm): vector loads and stores of 16-byte pieces, the
+// activations, and the launchers that the C entry points call.
+#pragma once
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// N elements of T moved as one access of N * sizeof(T) bytes.
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Vec {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Vec<T, N>& r, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = to_f32(r.v[i]);
+}
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> pack(const float (&f)[N]) {
+  Vec<T, N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(f[i]);
+  return r;
+}
+
+// 1 / (1 + e^-x).  __expf overflows to inf for x < -88, where the quotient is
+// zero as it should be.
+__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+__device__ __forceinline__ float activate(float x, int act) {
+  if (act == KDA_ACT_NONE) return x;
+  const float s = sigmoid_f32(x);
+  return act == KDA_ACT_SILU ? x * s : s;
+}
+
+// softplus(d) = log(1 + e^d) without overflow: max(d, 0) + log1p(e^-|d|).
+__device__ __forceinline__ float softplus_f32(float d) { return fmaxf(d, 0.f) + log1pf(expf(-fabsf(d))); }
+
+// Sequences of a token tensor: N of T tokens each, or packed by offsets.
+// Offsets are cut off at the tensor's T tokens, so that bad ones never lead
+// outside it.
+struct Seqs {
+  const int32_t* cu;
+  int N;
+  int64_t T;  // tokens per sequence, or in total when packed
+  __device__ __forceinline__ int64_t tokens() const { return cu ? T : (int64_t)N * T; }
+  __device__ __forceinline__ int64_t begin(int n) const {
+    if (!cu) return (int64_t)n * T;
+    const int64_t v = cu[n];
+    return v < 0 ? 0 : (v < T ? v : T);
+  }
+  __device__ __forceinline__ int64_t end(int n) const { return cu ? begin(n + 1) : (int64_t)(n + 1) * T; }
+  // The sequence that holds token t: the last n with begin(n) <= t (-1 when
+  // t lies before all of them; t >= end(n) when it lies behind the last).
+  __device__ __forceinline__ int find(int64_t t) const {
+    if (!cu) return (int)(t / T);
+    int lo = 0, hi = N;  // begin(lo - 1) <= t < begin(hi), taking begin(-1) = -inf
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (begin(mid) <= t) lo = mid + 1; else hi = mid;
+    }
+    return lo - 1;
+  }
+};
+
+struct ConvArgs {
+  const void* x;
+  int64_t ldx;
+  const float *weight, *bias;
+  const void* init;
+  void *out, *fin;
+  int N;
+  int64_t T;
+  int C, K;
+  const int32_t* cu;
+  int act;
+};
+cudaError_t launch_conv_fwd(const ConvArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& a, bool bf16, cudaStream_t s);  // N sequences; fin: the state, in place
+
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* gate;
+  int64_t ldg;
+  const float *weight, *bias;
+  void* out;
+  int64_t rows;
+  int groups, width, shared;
+  float eps;
+  int center, act, gate_first;
+};
+constexpr int NORM_MAX_WIDTH = 16384;
+cudaError_t launch_group_norm(const NormArgs& a, bool bf16, cudaStream_t s);
+
+struct SsmArgs {
+  const void* x;
+  int64_t ldx;
+  const void* b;
+  int64_t ldb;
+  const void* c;
+  int64_t ldc;
+  const float *delta, *A_log, *D, *dt_bias, *init;
+  void* out;
+  float* fin;
+  int N;      // sequences
+  int64_t T;  // tokens per sequence, or in total when packed
+  int H, G, dk, dv;
+  const int32_t* cu;
+  DeviceStatus* status;
+};
+cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmArgs& a, float* state, bool bf16, cudaStream_t s);
+
+// True when every row of `p` starts on a boundary of `bytes` (a power of two).
+inline bool rows_aligned(const void* p, int64_t ld, int esz, int bytes) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * esz) % bytes == 0);
+}
+
+}  // namespace kda

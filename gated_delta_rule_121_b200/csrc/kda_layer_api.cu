@@ -1,0 +1,147 @@
+// C entry points of the operators around a recurrent layer (declared in
+// include/kda.h): host-side validation and kernel dispatch.  Nothing here
+// allocates or synchronises.
+#include <cstdint>
+
+#include "../../include/kda.h"
+#include "kda_layer.cuh"
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;  // DeviceStatus + reserve, as in kda_fwd's workspace
+constexpr int kMaxChannels = 1 << 20;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool dtype_ok(kda_dtype_t dt) { return dt == KDA_F32 || dt == KDA_BF16; }
+int esize(kda_dtype_t dt) { return dt == KDA_BF16 ? 2 : 4; }
+kda_status_t result(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+kda_status_t check_conv(const void* x, int64_t ldx, const float* weight, const float* bias, const void* out, int C,
+                        int K, kda_act_t act, kda_dtype_t dt, bool empty) {
+  if (C <= 0 || ldx < C || !dtype_ok(dt)) return KDA_ERR_INVALID_ARG;
+  if (act != KDA_ACT_NONE && act != KDA_ACT_SILU) return KDA_ERR_INVALID_ARG;
+  if (K < 2 || K > 4 || C > kMaxChannels) return KDA_ERR_UNSUPPORTED;
+  if (!weight || (!empty && (!x || !out))) return KDA_ERR_INVALID_ARG;
+  if (!aligned_to(x, esize(dt))) return KDA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)weight, (const void*)bias, out})
+    if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+kda_status_t check_ssm(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
+                       const float* delta, const float* A_log, const float* D, const float* dt_bias, const void* out,
+                       int H, int G, int dk, int dv, kda_dtype_t dt, bool empty) {
+  if (H <= 0 || G <= 0 || H % G != 0 || !dtype_ok(dt)) return KDA_ERR_INVALID_ARG;
+  if (!dim_ok(dk) || !dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
+  if (ldx < (int64_t)H * dv || ldb < (int64_t)G * dk || ldc < (int64_t)G * dk) return KDA_ERR_INVALID_ARG;
+  for (int64_t ld : {ldx, ldb, ldc})
+    if (ld * esize(dt) % 16 != 0) return KDA_ERR_INVALID_ARG;
+  if (!A_log) return KDA_ERR_INVALID_ARG;
+  if (!empty && (!x || !b || !c || !delta || !out)) return KDA_ERR_INVALID_ARG;
+  if (!aligned_to(delta, 4)) return KDA_ERR_INVALID_ARG;
+  for (const void* p : {x, b, c, (const void*)A_log, (const void*)D, (const void*)dt_bias, out})
+    if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_conv_fwd(const void* x, int64_t ldx, const float* weight, const float* bias, const void* init_state,
+                          void* out, void* final_state, int B, int64_t T, int C, int K, const int32_t* cu_seqlens,
+                          kda_act_t act, void* stream, kda_dtype_t dt) {
+  if (B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
+  const int64_t tokens = cu_seqlens ? T : (T > INT32_MAX ? T : (int64_t)B * T);
+  if (T > (int64_t)INT32_MAX || tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  const kda_status_t st = check_conv(x, ldx, weight, bias, out, C, K, act, dt, tokens == 0 || B == 0);
+  if (st != KDA_OK) return st;
+  for (const void* p : {init_state, (const void*)final_state, (const void*)cu_seqlens})
+    if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+  if (B == 0) return KDA_OK;
+  const kda::ConvArgs a{x, ldx, weight, bias, init_state, out, final_state, B, T, C, K, cu_seqlens, act};
+  return result(kda::launch_conv_fwd(a, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t kda_conv_step(const void* x, int64_t ldx, const float* weight, const float* bias, void* state, void* out,
+                           int B, int C, int K, kda_act_t act, void* stream, kda_dtype_t dt) {
+  if (B < 0) return KDA_ERR_INVALID_ARG;
+  const kda_status_t st = check_conv(x, ldx, weight, bias, out, C, K, act, dt, B == 0);
+  if (st != KDA_OK) return st;
+  if ((B > 0 && !state) || !aligned16(state)) return KDA_ERR_INVALID_ARG;
+  if (B == 0) return KDA_OK;
+  const kda::ConvArgs a{x, ldx, weight, bias, nullptr, out, state, B, 1, C, K, nullptr, act};
+  return result(kda::launch_conv_step(a, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_ssm_fwd_workspace_size(int B, int64_t T, int H, int G, int dk, int dv, int packed, kda_dtype_t dt) {
+  (void)B; (void)T; (void)H; (void)G; (void)dk; (void)dv; (void)packed; (void)dt;
+  return kStatusBytes;
+}
+
+kda_status_t kda_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
+                         const float* delta, const float* A_log, const float* D, const float* dt_bias,
+                         const float* init_state, void* out, float* final_state, int B, int64_t T, int H, int G,
+                         int dk, int dv, const int32_t* cu_seqlens, void* stream, kda_dtype_t dt, void* workspace,
+                         size_t workspace_bytes) {
+  if (B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
+  if (T > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  const int64_t tokens = cu_seqlens ? T : (int64_t)B * T;
+  if (tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  const kda_status_t st =
+      check_ssm(x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, out, H, G, dk, dv, dt, tokens == 0 || B == 0);
+  if (st != KDA_OK) return st;
+  for (const void* p : {(const void*)init_state, (const void*)final_state, (const void*)cu_seqlens})
+    if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+  if ((int64_t)B * H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < kda_ssm_fwd_workspace_size(B, T, H, G, dk, dv, cu_seqlens != nullptr, dt))
+    return KDA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  kda::DeviceStatus* status = reinterpret_cast<kda::DeviceStatus*>(workspace);
+  if (cudaMemsetAsync(status, 0, sizeof(kda::DeviceStatus), s) != cudaSuccess) return KDA_ERR_CUDA;
+  if (B == 0) return KDA_OK;
+  const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state,
+                       B, T, H, G, dk, dv, cu_seqlens, status};
+  return result(kda::launch_ssm_fwd_simt(a, dt == KDA_BF16, s));
+}
+
+kda_status_t kda_ssm_step(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
+                          const float* delta, const float* A_log, const float* D, const float* dt_bias, float* state,
+                          void* out, int B, int H, int G, int dk, int dv, void* stream, kda_dtype_t dt) {
+  if (B < 0) return KDA_ERR_INVALID_ARG;
+  const kda_status_t st =
+      check_ssm(x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, out, H, G, dk, dv, dt, B == 0);
+  if (st != KDA_OK) return st;
+  if ((B > 0 && !state) || !aligned16(state)) return KDA_ERR_INVALID_ARG;
+  if ((int64_t)B * H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (B == 0) return KDA_OK;
+  const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, nullptr, out, nullptr,
+                       B, 1, H, G, dk, dv, nullptr, nullptr};
+  return result(kda::launch_ssm_step(a, state, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status_t kda_group_norm(const void* x, int64_t ldx, const void* gate, int64_t ldg, const float* weight,
+                            const float* bias, void* out, int64_t rows, int groups, int width, int shared, float eps,
+                            int center, kda_act_t act, int gate_first, void* stream, kda_dtype_t dt) {
+  if (rows < 0 || groups <= 0 || width <= 0 || !dtype_ok(dt) || !(eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+  if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID) return KDA_ERR_INVALID_ARG;
+  if (gate_first && !gate && rows > 0) return KDA_ERR_INVALID_ARG;
+  const int64_t C = (int64_t)groups * width;
+  if (ldx < C || (gate && ldg < C)) return KDA_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !out)) return KDA_ERR_INVALID_ARG;
+  if (!aligned_to(x, esize(dt)) || !aligned_to(gate, esize(dt))) return KDA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)weight, (const void*)bias, (const void*)out})
+    if (!aligned16(p) && p != x && p != gate) return KDA_ERR_INVALID_ARG;
+  // An output that is also an input is dense, so that every thread writes where it has read.
+  if (rows > 1 && ((out == x && ldx != C) || (out == gate && gate && ldg != C))) return KDA_ERR_INVALID_ARG;
+  if (width > kda::NORM_MAX_WIDTH || rows > (int64_t)INT32_MAX / groups) return KDA_ERR_UNSUPPORTED;
+  if (rows == 0) return KDA_OK;
+  const kda::NormArgs a{x, ldx, gate, ldg, weight, bias, out, rows, groups, width, shared ? 1 : 0,
+                        eps, center ? 1 : 0, act, gate_first ? 1 : 0};
+  return result(kda::launch_group_norm(a, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,255 @@
+// Selective state-space scan with a scalar decay per head, on CUDA cores: the
+// prompt form for fp32 inputs and for the sizes that the tensor-core kernel
+// does not take, and the single-token form for all of them.
+//
+//   D_t = softplus(delta_t + dt_bias),  a_t = exp(-exp(A_log) D_t)
+//   S_t = a_t S_{t-1} + D_t b_t x_t^T,  y_t = S_t^T c_t + D x_t
+//
+// Prompt: a block owns PV value columns of one head's state and walks its
+// sequence token by token.  A thread keeps NR rows of one column in registers;
+// the RG row groups of a column are neighbouring lanes, so y is a sum over RG
+// lanes.  TB tokens at a time are staged in shared memory as fp32 while the
+// next ones are on their way to registers.  The column's chain of multiply-adds
+// bounds it (4 dk dv flops per token and head).
+//
+// Single token: as the KDA decode step, the state is streamed once through
+// registers; HBM bandwidth bounds it (8 dk dv bytes per head).
+#include "kda_layer.cuh"
+
+namespace kda {
+namespace {
+
+template <int DK, int DV>
+struct ScanShape {
+  static constexpr int PV = DV < 32 ? DV : 32;        // columns per block
+  static constexpr int RG = DK >= 64 ? 8 : 4;         // row groups of a column
+  static constexpr int NR = DK / RG;                  // rows per thread, in float4 pieces
+  static constexpr int NT = PV * RG;                  // threads per block
+  static constexpr int TB = 16;                       // tokens per stage
+};
+
+template <int DK, int DV, typename IO>
+__global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
+    ssm_fwd_simt_kernel(const SsmArgs a) {
+  using Sh = ScanShape<DK, DV>;
+  constexpr int PV = Sh::PV, RG = Sh::RG, NR = Sh::NR, NT = Sh::NT, TB = Sh::TB;
+  __shared__ float s_x[2][TB][PV];
+  __shared__ alignas(16) float s_b[2][TB][DK], s_c[2][TB][DK];
+  __shared__ float s_a[2][TB], s_d[2][TB];
+  const int tid = threadIdx.x, rg = tid % RG, p = tid / RG;
+  const int h = blockIdx.x % a.H, n = blockIdx.x / a.H, col0 = blockIdx.y * PV;
+  const int grp = h / (a.H / a.G);
+  const Seqs q{a.cu, a.N, a.T};
+  const int64_t t0 = q.begin(n);
+  const int64_t L = q.end(n) - t0;
+  const IO* x = (const IO*)a.x + (int64_t)h * DV + col0;
+  const IO* b = (const IO*)a.b + (int64_t)grp * DK;
+  const IO* c = (const IO*)a.c + (int64_t)grp * DK;
+  IO* out = (IO*)a.out + (int64_t)h * DV + col0 + p;
+  const float rate = -expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.D ? a.D[h] : 0.f;
+
+  // Row j of piece k of this thread: 4 (rg + RG k) + j.
+  float s[NR];
+  const int64_t sbase = ((int64_t)n * a.H + h) * DK * DV + col0 + p;
+#pragma unroll
+  for (int k = 0; k < NR / 4; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      s[4 * k + j] = a.init ? a.init[sbase + (int64_t)(4 * (rg + RG * k) + j) * DV] : 0.f;
+
+  constexpr int XB = (TB * PV + NT - 1) / NT, KB = (TB * DK + NT - 1) / NT;
+  float rx[XB], rb[KB], rc[KB], rd = 0.f;
+  auto fetch = [&](int64_t at) {  // tokens [at, at + TB) to registers, zeros behind the end
+#pragma unroll
+    for (int i = 0; i < XB; ++i) {
+      const int e = tid + i * NT, t = e / PV;
+      rx[i] = (e < TB * PV && at + t < L) ? to_f32(x[(t0 + at + t) * a.ldx + e % PV]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      const int e = tid + i * NT, t = e / DK;
+      const bool in = e < TB * DK && at + t < L;
+      rb[i] = in ? to_f32(b[(t0 + at + t) * a.ldb + e % DK]) : 0.f;
+      rc[i] = in ? to_f32(c[(t0 + at + t) * a.ldc + e % DK]) : 0.f;
+    }
+    if (tid < TB && at + tid < L) rd = a.delta[(t0 + at + tid) * a.H + h];
+  };
+  auto stage = [&](int buf, int64_t at) {
+#pragma unroll
+    for (int i = 0; i < XB; ++i) {
+      const int e = tid + i * NT;
+      if (e < TB * PV) (&s_x[buf][0][0])[e] = rx[i];
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      const int e = tid + i * NT;
+      if (e < TB * DK) {
+        (&s_b[buf][0][0])[e] = rb[i];
+        (&s_c[buf][0][0])[e] = rc[i];
+      }
+    }
+    if (tid < TB) {
+      const float d = at + tid < L ? (a.dt_bias ? softplus_f32(rd + bias) : rd) : 0.f;
+      s_d[buf][tid] = d;
+      s_a[buf][tid] = expf(rate * d);
+    }
+  };
+  if (L > 0) {
+    fetch(0);
+    stage(0, 0);
+  }
+  __syncthreads();
+  for (int64_t at = 0; at < L; at += TB) {
+    const int buf = (int)(at / TB) & 1;
+    if (at + TB < L) fetch(at + TB);
+    const int m = (int)(L - at < TB ? L - at : TB);
+#pragma unroll 4
+    for (int t = 0; t < m; ++t) {
+      const float xv = s_x[buf][t][p], dx = s_d[buf][t] * xv, av = s_a[buf][t];
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < NR / 4; ++k) {
+        const float4 bv = *reinterpret_cast<const float4*>(&s_b[buf][t][4 * (rg + RG * k)]);
+        const float4 cv = *reinterpret_cast<const float4*>(&s_c[buf][t][4 * (rg + RG * k)]);
+        const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[4 * k + j] = fmaf(av, s[4 * k + j], bb[j] * dx);
+          y = fmaf(s[4 * k + j], cc[j], y);
+        }
+      }
+#pragma unroll
+      for (int o = RG / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      if (rg == 0) out[(t0 + at + t) * ((int64_t)a.H * DV)] = from_f32<IO>(fmaf(skip, xv, y));
+    }
+    if (at + TB < L) stage(buf ^ 1, at + TB);
+    __syncthreads();
+  }
+  if (a.fin) {
+#pragma unroll
+    for (int k = 0; k < NR / 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a.fin[sbase + (int64_t)(4 * (rg + RG * k) + j) * DV] = s[4 * k + j];
+  }
+}
+
+template <int DK, int DV>
+struct StepShape {
+  static constexpr int COLQ = DV / 4;                               // float4 column groups
+  static constexpr int RG = (256 / COLQ) < DK ? (256 / COLQ) : DK;  // row groups
+  static constexpr int ROWS = DK / RG;                              // rows per thread
+  static constexpr int NT = COLQ * RG;                              // threads per block
+};
+
+template <int DK, int DV, typename IO>
+__global__ void __launch_bounds__(StepShape<DK, DV>::NT)
+    ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
+  using Sh = StepShape<DK, DV>;
+  constexpr int COLQ = Sh::COLQ, RG = Sh::RG, ROWS = Sh::ROWS;
+  __shared__ float s_b[DK], s_c[DK];
+  __shared__ float4 s_y[RG][COLQ];
+  const int tid = threadIdx.x, cq = tid % COLQ, rg = tid / COLQ;
+  const int64_t bh = blockIdx.x;
+  const int h = (int)(bh % a.H);
+  const int64_t n = bh / a.H;
+  float4* S = reinterpret_cast<float4*>(state + bh * DK * DV);
+  // The state's loads go first; the token is staged while they are in flight.
+  float4 s[ROWS];
+#pragma unroll
+  for (int m = 0; m < ROWS; ++m) s[m] = __ldcs(S + (rg * ROWS + m) * COLQ + cq);
+  const int grp = h / (a.H / a.G);
+  const IO* b = (const IO*)a.b + n * a.ldb + (int64_t)grp * DK;
+  const IO* c = (const IO*)a.c + n * a.ldc + (int64_t)grp * DK;
+  const IO* xp = (const IO*)a.x + n * a.ldx + (int64_t)h * DV + 4 * cq;
+  for (int i = tid; i < DK; i += Sh::NT) {
+    s_b[i] = to_f32(b[i]);
+    s_c[i] = to_f32(c[i]);
+  }
+  float d = a.delta[bh];
+  if (a.dt_bias) d = softplus_f32(d + a.dt_bias[h]);
+  const float av = expf(-expf(a.A_log[h]) * d), skip = a.D ? a.D[h] : 0.f;
+  const float4 x = make_float4(to_f32(xp[0]), to_f32(xp[1]), to_f32(xp[2]), to_f32(xp[3]));
+  const float4 dx = make_float4(d * x.x, d * x.y, d * x.z, d * x.w);
+  __syncthreads();
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int m = 0; m < ROWS; ++m) {
+    const int i = rg * ROWS + m;
+    const float bi = s_b[i], ci = s_c[i];
+    s[m].x = fmaf(av, s[m].x, bi * dx.x);
+    s[m].y = fmaf(av, s[m].y, bi * dx.y);
+    s[m].z = fmaf(av, s[m].z, bi * dx.z);
+    s[m].w = fmaf(av, s[m].w, bi * dx.w);
+    y.x = fmaf(s[m].x, ci, y.x);
+    y.y = fmaf(s[m].y, ci, y.y);
+    y.z = fmaf(s[m].z, ci, y.z);
+    y.w = fmaf(s[m].w, ci, y.w);
+    __stcs(S + i * COLQ + cq, s[m]);
+  }
+  s_y[rg][cq] = y;
+  __syncthreads();
+  if (rg == 0) {
+#pragma unroll
+    for (int r = 1; r < RG; ++r) {
+      const float4 v = s_y[r][cq];
+      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+    }
+    IO* o = (IO*)a.out + bh * DV + 4 * cq;
+    o[0] = from_f32<IO>(fmaf(skip, x.x, y.x));
+    o[1] = from_f32<IO>(fmaf(skip, x.y, y.y));
+    o[2] = from_f32<IO>(fmaf(skip, x.z, y.z));
+    o[3] = from_f32<IO>(fmaf(skip, x.w, y.w));
+  }
+}
+
+struct Fwd {
+  template <int DK, int DV, typename IO>
+  static cudaError_t go(const SsmArgs& a, float*, cudaStream_t s) {
+    using Sh = ScanShape<DK, DV>;
+    ssm_fwd_simt_kernel<DK, DV, IO><<<dim3((unsigned)(a.N * a.H), DV / Sh::PV), Sh::NT, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
+struct Step {
+  template <int DK, int DV, typename IO>
+  static cudaError_t go(const SsmArgs& a, float* state, cudaStream_t s) {
+    ssm_step_kernel<DK, DV, IO><<<(unsigned)((int64_t)a.N * a.H), StepShape<DK, DV>::NT, 0, s>>>(a, state);
+    return cudaGetLastError();
+  }
+};
+
+template <typename F, int DK, int DV>
+cudaError_t by_type(const SsmArgs& a, float* state, bool bf16, cudaStream_t s) {
+  return bf16 ? F::template go<DK, DV, __nv_bfloat16>(a, state, s) : F::template go<DK, DV, float>(a, state, s);
+}
+template <typename F, int DK>
+cudaError_t by_dv(const SsmArgs& a, float* state, bool bf16, cudaStream_t s) {
+  switch (a.dv) {
+    case 16: return by_type<F, DK, 16>(a, state, bf16, s);
+    case 32: return by_type<F, DK, 32>(a, state, bf16, s);
+    case 64: return by_type<F, DK, 64>(a, state, bf16, s);
+    case 128: return by_type<F, DK, 128>(a, state, bf16, s);
+  }
+  return cudaErrorInvalidValue;
+}
+template <typename F>
+cudaError_t by_dims(const SsmArgs& a, float* state, bool bf16, cudaStream_t s) {
+  switch (a.dk) {
+    case 16: return by_dv<F, 16>(a, state, bf16, s);
+    case 32: return by_dv<F, 32>(a, state, bf16, s);
+    case 64: return by_dv<F, 64>(a, state, bf16, s);
+    case 128: return by_dv<F, 128>(a, state, bf16, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, bool bf16, cudaStream_t s) {
+  return by_dims<Fwd>(a, nullptr, bf16, s);
+}
+cudaError_t launch_ssm_step(const SsmArgs& a, float* state, bool bf16, cudaStream_t s) {
+  return by_dims<Step>(a, state, bf16, s);
+}
+
+}  // namespace kda

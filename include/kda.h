@@ -438,6 +438,128 @@ KDA_API kda_status_t kda_decode_spec_gated(const void *q_prev, const void *k_pre
                                            float *state, void *out, int B, int Wp, int W, int H, int dk, int dv,
                                            void *stream, kda_dtype_t dt);
 
+/* ------------------------------------------------------------------------
+ * The operators around a recurrent layer.  The digest's "Kimi Delta
+ * Attention" section names two of them for a KDA layer (a short convolution
+ * of kernel size 4 with a Swish on q, k and v before the recurrence; a
+ * per-head RMSNorm with a sigmoid gate after it), and hybrid stacks use the
+ * same two around a selective state-space scan, whose per-head state has the
+ * layout and the serving forms of the KDA state.  Forward only, like the rest
+ * of the library.
+ *
+ * Unlike the entry points above these take row strides for their token
+ * tensors, so that slices of one fused projection or of one convolution's
+ * output are read where they lie: `ldx` is the distance in elements between
+ * consecutive tokens (sequence b, token t is row b*T + t), at least the
+ * row's own width.  Outputs, states and parameters are dense.  Parameters
+ * (weights, biases, A_log, D, dt_bias), delta and recurrent states are fp32.
+ * The convolution's x, the norm's x and gate, and delta may start at any element;
+ * every other pointer is 16-byte aligned as above.
+ * --------------------------------------------------------------------- */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 } kda_act_t;
+
+/*
+ * Short depthwise causal convolution over whole sequences, with an optional
+ * activation (KDA_ACT_NONE or KDA_ACT_SILU):
+ *   out_t[c] = act( bias[c] + sum_{j<K} weight[c][j] x_{t-K+1+j}[c] )
+ * where inputs before a sequence's first token are the rows of its initial
+ * state (zeros without one).
+ *   x          [B, T, C]     dtype dt, row stride ldx >= C
+ *   weight     [C, K] fp32;  bias [C] fp32 or NULL;  K in {2, 3, 4}
+ *   init_state [N, K-1, C]   dtype dt or NULL: the K-1 inputs before each
+ *              sequence, oldest first
+ *   out        [B, T, C]     dtype dt, dense; must not overlap x
+ *   final_state[N, K-1, C]   dtype dt or NULL: the last K-1 inputs (rows of
+ *              init_state, or zeros, where a sequence is shorter than K-1);
+ *              may be init_state itself
+ *   cu_seqlens as in kda_fwd (packed: x is [1, T, C], B = N).  Rows outside
+ *              [cu[0], cu[N]) are neither read for another sequence nor written.
+ * Sums are fp32, rounded once.  No workspace.
+ */
+KDA_API kda_status_t kda_conv_fwd(const void *x, int64_t ldx, const float *weight, const float *bias,
+                                  const void *init_state, void *out, void *final_state, int B, int64_t T,
+                                  int C, int K, const int32_t *cu_seqlens, kda_act_t act, void *stream,
+                                  kda_dtype_t dt);
+
+/*
+ * One token of the same convolution for each of B sequences: the state is
+ * shifted by one row in place, the new input becomes its last row.
+ *   x [B, C] dtype dt, row stride ldx;  state [B, K-1, C] dtype dt, in place;
+ *   out [B, C] dtype dt, dense.  B = 0 is a no-op.  No workspace.
+ */
+KDA_API kda_status_t kda_conv_step(const void *x, int64_t ldx, const float *weight, const float *bias,
+                                   void *state, void *out, int B, int C, int K, kda_act_t act, void *stream,
+                                   kda_dtype_t dt);
+
+/*
+ * Selective state-space scan over whole sequences (scalar decay per head):
+ *   D_t = softplus(delta_t + dt_bias[h])   (delta_t itself when dt_bias is NULL)
+ *   a_t = exp(-exp(A_log[h]) D_t)
+ *   S_t = a_t S_{t-1} + D_t b_t x_t^T            (dk x dv)
+ *   y_t = S_t^T c_t + D[h] x_t
+ * Head h reads b and c of group h / (H / G).
+ *   x       [B, T, H, dv]  dtype dt, row stride ldx (elements between tokens)
+ *   b, c    [B, T, G, dk]  dtype dt, row strides ldb, ldc;  H % G == 0
+ *   delta   [B, T, H] fp32, dense; finite, and >= 0 when dt_bias is NULL
+ *   A_log   [H] fp32;  D [H], dt_bias [H] fp32 or NULL
+ *   init_state, final_state [N, H, dk, dv] fp32 or NULL, as in kda_fwd
+ *              (final_state may be init_state itself)
+ *   out     [B, T, H, dv]  dtype dt, dense
+ *   cu_seqlens as in kda_fwd; rows outside [cu[0], cu[N]) are not written.
+ *   dk, dv in {16, 32, 64, 128}.  ldx, ldb, ldc times the element size must
+ *   be multiples of 16 bytes (KDA_ERR_INVALID_ARG).
+ *   workspace  at least kda_ssm_fwd_workspace_size(...) bytes (packed: nonzero
+ *              with cu_seqlens, T then the total token count and B = N).  Its
+ *              contents on entry do not matter; kda_workspace_status reads
+ *              its status word.
+ * fp32 inputs, and sizes other than dk, dv in {64, 128}, run in fp32 on CUDA
+ * cores; bf16 with dk, dv in {64, 128} runs on the tensor cores with bf16
+ * operands and fp32 accumulation (any bf16 magnitude; the state itself is
+ * fp32 and the operands that update it carry 24 bits).  A non-finite input
+ * spoils the outputs of its own sequence only: from its 64-token chunk on.
+ */
+KDA_API size_t kda_ssm_fwd_workspace_size(int B, int64_t T, int H, int G, int dk, int dv, int packed,
+                                          kda_dtype_t dt);
+KDA_API kda_status_t kda_ssm_fwd(const void *x, int64_t ldx, const void *b, int64_t ldb, const void *c,
+                                 int64_t ldc, const float *delta, const float *A_log, const float *D,
+                                 const float *dt_bias, const float *init_state, void *out,
+                                 float *final_state, int B, int64_t T, int H, int G, int dk, int dv,
+                                 const int32_t *cu_seqlens, void *stream, kda_dtype_t dt, void *workspace,
+                                 size_t workspace_bytes);
+
+/*
+ * One token of the same scan for each of B sequences, the state updated in
+ * place.  x [B, H, dv], b, c [B, G, dk] with row strides; delta [B, H];
+ * state [B, H, dk, dv] fp32; out [B, H, dv].  B = 0 is a no-op.  No workspace.
+ */
+KDA_API kda_status_t kda_ssm_step(const void *x, int64_t ldx, const void *b, int64_t ldb, const void *c,
+                                  int64_t ldc, const float *delta, const float *A_log, const float *D,
+                                  const float *dt_bias, float *state, void *out, int B, int H, int G, int dk,
+                                  int dv, void *stream, kda_dtype_t dt);
+
+/*
+ * Group norm over the channels of each row (token), channels last, with an
+ * activation: a row's groups * width channels are normalised group by group
+ * (a group is a head in a KDA layer).
+ *   u = x                     or, with gate_first, x act(gate)
+ *   n = (u - mu) / sqrt(mean((u - mu)^2) + eps) * weight + bias,
+ *       mu the group's mean with `center`, 0 without (the RMS form)
+ *   out = n act(gate)         with a gate,
+ *         n                   with a gate and gate_first,
+ *         act(n)              without a gate
+ *   x, gate [rows, groups*width] dtype dt, row strides ldx, ldg; gate may be NULL
+ *   weight, bias  fp32 or NULL (ones, zeros): [groups*width], or [width] shared
+ *           by all groups when `shared` is nonzero
+ *   out     [rows, groups*width] dtype dt, dense; may be x or gate itself when
+ *           that one is dense (each element is read before it is written)
+ * Statistics are two-pass (mean, then centred squares) in fp32.  width <= 16384.
+ * No workspace.
+ */
+KDA_API kda_status_t kda_group_norm(const void *x, int64_t ldx, const void *gate, int64_t ldg,
+                                    const float *weight, const float *bias, void *out, int64_t rows,
+                                    int groups, int width, int shared, float eps, int center, kda_act_t act,
+                                    int gate_first, void *stream, kda_dtype_t dt);
+
 /*
  * Read back the device status word of a workspace used by kda_fwd.
  * Synchronises `stream` (it is the one call that does) and returns KDA_OK or
