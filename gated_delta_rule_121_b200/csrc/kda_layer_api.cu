@@ -77,8 +77,9 @@ kda_status_t kda_conv_step(const void* x, int64_t ldx, const float* weight, cons
 }
 
 size_t kda_ssm_fwd_workspace_size(int B, int64_t T, int H, int G, int dk, int dv, int packed, kda_dtype_t dt) {
-  (void)B; (void)T; (void)H; (void)G; (void)dk; (void)dv; (void)packed; (void)dt;
-  return kStatusBytes;
+  if (B <= 0 || T <= 0 || H <= 0 || G <= 0 || H % G != 0 || !kda::ssm_tc_supported(dk, dv, dt == KDA_BF16))
+    return kStatusBytes;
+  return kda::ssm_tc_workspace(B, T, H, G, dk, dv, packed != 0);
 }
 
 kda_status_t kda_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
@@ -105,6 +106,7 @@ kda_status_t kda_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb,
   if (B == 0) return KDA_OK;
   const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state,
                        B, T, H, G, dk, dv, cu_seqlens, status};
+  if (tokens > 0 && kda::ssm_tc_supported(dk, dv, dt == KDA_BF16)) return result(kda::launch_ssm_fwd_tc(a, workspace, s));
   return result(kda::launch_ssm_fwd_simt(a, dt == KDA_BF16, s));
 }
 
