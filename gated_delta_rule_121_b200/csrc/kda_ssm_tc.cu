@@ -27,13 +27,10 @@
 // output's products as bf16 (half a step each, 2^-8 relative): y is rounded to
 // bf16 itself, and the three are of one size.
 //
-// Roles (23 warps, one block per SM): wx (4 warps) weights x and stores its
-// terms; scores (4) turn G into M; state (8) holds S; out (4) combines YI, YM
-// and the skip and stores y by TMA from x's own tile; one warp each for the
-// loads, the MMA issue and the chunk's scalars.  The MMAs of a chunk take
-// ~1500 cycles of tensor pipe at dv = 64 (half of it U's three terms); the
-// other roles' instructions per chunk stay below that, so the tensor pipe is
-// the bound that the layout aims at.
+// Roles (32 warps, one block per SM): wx (4 warps) weights x and stores its
+// terms; scores and outputs (8) turn G into M and combine YI, YM and the skip
+// over x's own tile; state (16) holds S; one warp each for the copies, the
+// issue of U, that of the other products, and the chunk's scalars.
 //
 // Pieces.  A sequence longer than the plan's piece length is cut into pieces
 // that run in parallel: a first pass (states only) gives each piece's own state
@@ -49,74 +46,82 @@ namespace {
 
 constexpr int CH = 64;       // tokens per chunk
 constexpr int PT = 128;      // value columns per tile
-constexpr int NST = 3;       // stages of x, b, c
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // limit of every in-kernel wait
 
-constexpr int W_WX = 0, W_SC = 4, W_OUT = 8, W_ST = 12, W_TMA = 20, W_MMA = 21, W_DEC = 22, NWARP = 23;
+constexpr int W_WX = 0, W_SO = 4, W_ST = 12, ST_WARPS = 16, W_MOVE = W_ST + ST_WARPS, W_MMY = W_MOVE + 1, W_MMU = W_MOVE + 2, W_DEC = W_MOVE + 3,
+              NWARP = W_MOVE + 4;
 constexpr int NTHR = 32 * NWARP;
-enum { GRP_WX = 1, GRP_SC, GRP_OUT, GRP_ST };  // named barriers
+enum { GRP_WX = 1 };  // named barrier
 
+// Stages: x and the scalars share a ring of NX, b and c have one of NB (they
+// are released earlier).
+constexpr int MAXST = 6;
 enum Bar {
-  B_FULL0 = 0, B_DEC0 = B_FULL0 + NST, B_EMPTY0 = B_DEC0 + NST, B_WX = B_EMPTY0 + NST, B_U, B_UFREE, B_G, B_GFREE,
-  B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE, B_DRAIN, NUM_BARS
+  B_XFULL = 0, B_XFREE = B_XFULL + MAXST, B_DEC = B_XFREE + MAXST, B_KFULL = B_DEC + MAXST, B_YOUT = B_KFULL + MAXST, B_XREAD = B_YOUT + MAXST,
+  B_KFREE = B_XREAD + MAXST,
+  B_WX0 = B_KFREE + MAXST, B_WX1, B_U0, B_U1, B_UFREE, B_G, B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE,
+  B_DRAIN, NUM_BARS
 };
 
-// Scalars of a chunk, per head: floats at these offsets.
-constexpr int SC_W = 0, SC_CUM = 64, SC_D = 128, SC_ECUM = 192, SC_ER = 256, SC_ECD = 320, SC_FLOATS = 512;
-// SC_W e^{G_C - G_s} D_s; SC_CUM G_t (log2); SC_D D_s; SC_ECUM e^{G_t}; SC_ER e^{G_t - R_q} with R_q = G before the
-// 16-token block q of t; SC_ECD + 64 (q - 1): e^{R_q - G_s} D_s for s before block q.
+// Scalars of a chunk, per head, at these 32-bit words: the steps D_s; the
+// weights w_s = e^{G_C - G_s} D_s as three bf16 terms (pairs of tokens, 32 words
+// each); G_t; G_s - log D_s (both in log2 units).
+constexpr int SC_D = 0, SC_W = 64, SC_CUM = 160, SC_LS = 224;
 
-template <int DK, int DV>
+template <int DK, int DV, bool STATES>
 struct Cfg {
   static constexpr int HEADS = PT / DV;                  // heads per tile, at most
-  static constexpr uint32_t KV_BYTES = CH * DK * 2;      // b or c of a chunk
-  static constexpr uint32_t X_BYTES = CH * PT * 2;
-  static constexpr uint32_t STAGE = X_BYTES + 2 * KV_BYTES;
-  static constexpr uint32_t M_BYTES = CH * CH * 2;       // one head's scores
-  static constexpr uint32_t ZERO = 2048;                 // 16 rows of zeros of 64 columns
-  // shared memory: zeros, the stages, zeros (the zero tiles lie below and above x: descriptor strides are positive)
-  static constexpr uint32_t SM_Z0 = 0, SM_STAGE = ZERO, SM_Z1 = SM_STAGE + NST * STAGE, SM_M = SM_Z1 + ZERO;
-  static constexpr uint32_t SM_DEC = SM_M + 2 * HEADS * M_BYTES;
-  static constexpr uint32_t SM_MISC = SM_DEC + NST * HEADS * SC_FLOATS * 4;
-  static constexpr uint32_t BYTES = SM_MISC + 512 + 1024;
+  static constexpr int NX = STATES ? 6 : 4, NB = STATES ? 6 : 3;
+  static constexpr uint32_t KV = CH * DK * 2;            // b or c of a chunk
+  static constexpr uint32_t X_BYTES = CH * PT * 2, K_BYTES = STATES ? KV : 2 * KV;
+  static constexpr uint32_t M_BYTES = STATES ? 0 : CH * CH * 2;  // one head's scores
+  static constexpr uint32_t ZERO = STATES ? 0 : 2048;            // 16 rows of zeros of 64 columns
+  static constexpr int SC_FLOATS = STATES ? 160 : 288, SC_SLOT = HEADS * SC_FLOATS * 4;
+  // shared memory: zeros, x, zeros (the zero tiles lie below and above x: descriptor strides are positive)
+  static constexpr uint32_t SM_Z0 = 0, SM_X = ZERO, SM_Z1 = SM_X + NX * X_BYTES, SM_K = SM_Z1 + ZERO;
+  static constexpr uint32_t SM_M = SM_K + NB * K_BYTES, SM_DEC = SM_M + 2 * HEADS * M_BYTES;
+  static constexpr uint32_t SM_RAW = SM_DEC + NX * SC_SLOT;  // delta of four chunks to come
+  static constexpr uint32_t SM_MISC = SM_RAW + 4 * HEADS * CH * 4;
+  static constexpr uint32_t BYTES = SM_MISC + 1024 + 1024;
   // TMEM columns
-  static constexpr uint32_t TM_WX = 0, TM_S = 96, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64, TM_U = TM_YM + 64,
+  static constexpr uint32_t TM_WX = 0, TM_S = 128, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64, TM_U = TM_YM + 64,
                             TM_G = TM_U + DK, TM_END = TM_G + 64;
   static constexpr uint32_t TM_COLS = 512;
+  static_assert(NX <= MAXST && NB <= MAXST, "stages");
   static_assert(TM_END <= TM_COLS, "TMEM");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
-constexpr uint32_t MS_TMEM = 384, MS_ABORT = 388, MS_TOTAL = 392;  // in SM_MISC, behind the barriers
+// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot and head.
+constexpr uint32_t MS_TMEM = 512, MS_ABORT = 516, MS_TOTAL = 528;
 static_assert(NUM_BARS * 8 <= MS_TMEM, "barrier area");
 
 // ------------------------------------------------------------------ PTX
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1) {
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      "l"(tmap), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap), "r"(src),
                "r"(c0), "r"(c1)
                : "memory");
 }
-// 16 lanes x 16 columns (fp32): thread l gets rows l/4 and l/4 + 8, of each 8
+// 16 lanes x 32 columns (fp32): thread l gets rows l/4 and l/4 + 8, of each 8
 // columns numbers 2 (l % 4) and the next: {r, c}, {r, c+1}, {r+8, c}, {r+8, c+1},
-// then the same of the next 8 columns.  Not waited for.
-__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-               : "r"(taddr));
-}
-// Waits for this thread's TMEM loads; ties 16 of their registers to the wait.
-__device__ __forceinline__ void tmem_wait_ld(float (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
-               :
-               : "memory");
+// then the same of the next 8 columns, and so on.
+__device__ __forceinline__ void tmem_ld_16x256b_x4_wait(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
   asm volatile(
@@ -125,6 +130,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
         "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr)
+      : "memory");
+}
+// 32 columns from each of two places.
+__device__ __forceinline__ void tmem_ld_16x256b_x4x2_wait(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(a[8]),
+        "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]), "=f"(b[0]), "=f"(b[1]),
+        "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]),
+        "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15])
+      : "r"(ta), "r"(tb)
       : "memory");
 }
 // 16 lanes x 16 columns of 32-bit values, row l/4 (and + 8), column l % 4 of each 4.
@@ -160,6 +178,32 @@ __device__ __forceinline__ void stsm_x4(uint32_t saddr, const uint32_t (&r)[4]) 
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_f16_f32(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);  // A, B format 1 = bf16
 }
+// MMAs whose descriptors differ in their low words only (address and atom
+// stride, both in 16-byte units): 128-byte swizzle, 1024 bytes between groups
+// of 8 rows, the sm_100 descriptor version.
+constexpr uint32_t DESC_HI = (2u << 29) | (1u << 14) | (1024u >> 4);
+__device__ __forceinline__ void umma_ss_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(DESC_HI)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(DESC_HI)
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float2 bf16x2_f32(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
@@ -167,11 +211,26 @@ __device__ __forceinline__ float2 bf16x2_f32(uint32_t u) {
 __device__ __forceinline__ uint32_t upper_halves(float2 v) {
   return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
 }
-__device__ __forceinline__ float2 minus_upper(float2 v) {  // exact
+__device__ __forceinline__ float2 below_upper(float2 v) {  // what that leaves, exactly
   return make_float2(v.x - __uint_as_float(__float_as_uint(v.x) & 0xffff0000u),
                      v.y - __uint_as_float(__float_as_uint(v.y) & 0xffff0000u));
 }
-
+// Packed bf16 arithmetic, rounded to nearest.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t fms_bf16x2(uint32_t a, uint32_t b, uint32_t c) {  // a b - c
+  uint32_t d;
+  asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %3;\n\tfma.rn.bf16x2 %0, %1, %2, n;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 // ------------------------------------------------------------------ pieces
 // One piece of a sequence: tokens [start, end) of sequence n, its r-th piece
 // of `pieces`.  A sequence of several pieces has `pieces` slots for states from
@@ -259,362 +318,600 @@ __global__ void __launch_bounds__(1024) ssm_piece_table_kernel(Seqs q, int64_t p
 }
 
 // ------------------------------------------------------------------ roles
+// Every role walks all chunks, so each block runs seven programs at once.  Their
+// loops are kept rolled and short: the instruction caches hold all of them only
+// then (with the roles unrolled, warps waited for instructions most of the
+// time, 3.6 us a chunk).
 struct Ctx {
   uint8_t* sm;
-  uint32_t sb, tmem;
-  uint64_t* bars;
-  volatile int* abort;
-  DeviceStatus* status;
+  uint32_t sb, tmem, bars;   // shared-window addresses of sm and of the barriers; TMEM base
   Piece piece;
-  int h0, heads, tile;   // first head of the tile, heads in it
+  int h0, heads, tile;       // first head of the tile, heads in it
   int nchunks;
 };
 
-// Bounded wait that also gives up once another role has.
-__device__ __forceinline__ bool wait_bar(const Ctx& x, int bar, uint32_t parity) {
-  uint64_t* b = &x.bars[bar];
-  if (mbar_try_wait(b, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(b, parity)) {
-    if (*x.abort) return false;
-    if (globaltimer_ns() - t0 > WAIT_NS) {
-      *x.abort = 1;
-      record_error(x.status, KDA_ERR_TIMEOUT, bar);
+// Tests a phase; the thread may sleep meanwhile (up to the hint, in ns).
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait that also gives up once another role has: the first to give up
+// raises the block's flag, and from then on no wait of the block waits long.
+// The roles that only compute run on over whatever is there (every access stays
+// inside its buffers); the ones that start copies or products stop.
+__device__ __noinline__ bool wait_long(uint32_t bars, uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t polls = 0; !try_wait(bar, parity); ++polls) {
+    if ((polls & 15) != 15) continue;
+    uint32_t abort;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(abort) : "r"(bars + MS_ABORT) : "memory");
+    if (t0 == 0) t0 = globaltimer_ns();
+    if (abort != 0 || globaltimer_ns() - t0 > WAIT_NS) {
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(bars + MS_ABORT), "r"(1u) : "memory");
       return false;
     }
   }
   return true;
 }
+__device__ __forceinline__ bool wait_bar(const Ctx& x, int bar, uint32_t parity) {
+  const uint32_t b = x.bars + 8 * bar;
+  if (try_wait(b, parity)) return true;
+  return wait_long(x.bars, b, parity);
+}
+__device__ __forceinline__ void arrive(const Ctx& x, int bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(x.bars + 8 * bar) : "memory");
+}
+__device__ __forceinline__ void commit(const Ctx& x, int bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(x.bars + 8 * bar)
+               : "memory");
+}
 __device__ __forceinline__ int valid_rows(const Ctx& x, int i) {
-  const int64_t left = x.piece.end - x.piece.start - (int64_t)i * CH;
-  return left < CH ? (int)left : CH;
+  const int left = (int)(x.piece.end - x.piece.start) - i * CH;
+  return left < CH ? left : CH;
 }
-
-template <int DK, int DV, bool STATES>
-__device__ __forceinline__ void role_load(const Ctx& x, const void* tx, const void* tb, const void* tc, int group) {
-  using K = Cfg<DK, DV>;
-  int issued = 0;
-  for (int i = 0; i < x.nchunks; ++i) {
-    const int st = i % NST;
-    if (i >= NST && !wait_bar(x, B_EMPTY0 + st, (i / NST - 1) & 1)) break;
-    uint64_t* bar = &x.bars[B_FULL0 + st];
-    const uint32_t stg = x.sb + K::SM_STAGE + st * K::STAGE;
-    const int tok = (int)(x.piece.start + (int64_t)i * CH);
-    const int atoms = x.heads * DV / 64;
-    mbar_arrive_expect_tx(bar, atoms * 8192 + (STATES ? 1 : 2) * K::KV_BYTES);
-    for (int k = 0; k < DK / 64; ++k) {
-      tma_load_2d(stg + K::X_BYTES + k * 8192, tb, bar, group * DK + 64 * k, tok);
-      if (!STATES) tma_load_2d(stg + K::X_BYTES + K::KV_BYTES + k * 8192, tc, bar, group * DK + 64 * k, tok);
-    }
-    for (int k = 0; k < atoms; ++k) tma_load_2d(stg + k * 8192, tx, bar, x.h0 * DV + 64 * k, tok);
-    issued = i + 1;
+// A copy or product in flight has ended, whatever else the block gave up.
+__device__ __forceinline__ void land(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait(bar, parity) && globaltimer_ns() - t0 < WAIT_NS) {
   }
-  // No load stays in flight behind the block.
-  for (int i = issued > NST ? issued - NST : 0; i < issued; ++i) mbar_wait(&x.bars[B_FULL0 + i % NST], (i / NST) & 1, WAIT_NS);
 }
-
-template <int DK, int DV, bool STATES>
-__device__ __forceinline__ void role_mma(const Ctx& x) {
-  using K = Cfg<DK, DV>;
-  auto stage = [&](int i) { return x.sb + K::SM_STAGE + (i % NST) * K::STAGE; };
-  auto scores = [&](int i) {  // G of chunk i
-    const uint32_t b = stage(i) + K::X_BYTES, c = b + K::KV_BYTES;
-    const uint32_t id = idesc_bf16_f32(64, 64, 0, 0);
-#pragma unroll
-    for (int k = 0; k < DK / 16; ++k) {
-      const uint32_t o = (k >> 2) * 8192 + (k & 3) * 32;
-      umma_ss(x.tmem + K::TM_G, sdesc_sw128(c + o, 16, 1024), sdesc_sw128(b + o, 16, 1024), id, k > 0);
+// A chunk's stage in a ring of N and the parity of its use, counted along.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
     }
-    umma_commit(&x.bars[B_G]);
+  }
+};
+
+// Loads, and the stores of y out of x's tile: by TMA, or row by row where the
+// sequence's end cuts the last chunk short.  A stage of x is loaded anew once
+// its y has been read for the store.
+template <int DK, int DV, bool STATES>
+__device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const void* tx, const void* tb, const void* tc,
+                                          const void* to, bool leader) {
+  using K = Cfg<DK, DV, STATES>;
+  const int atoms = x.heads * DV / 64, group = x.h0 / (t.a.H / t.a.G), col = x.h0 * DV, tok0 = (int)x.piece.start;
+  int nk = 0, nx = 0;  // chunks whose loads have been issued
+  Ring<K::NB> k;
+  Ring<K::NX> s;
+  auto load_k = [&]() {
+    if (leader) {
+      const uint32_t bar = x.bars + 8 * (B_KFULL + k.st), dst = x.sb + K::SM_K + k.st * K::K_BYTES;
+      expect_tx(bar, K::K_BYTES);
+#pragma unroll
+      for (int e = 0; e < DK / 64; ++e) {
+        tma_load_2d(dst + e * 8192, tb, bar, group * DK + 64 * e, tok0 + nk * CH);
+        if (!STATES) tma_load_2d(dst + K::KV + e * 8192, tc, bar, group * DK + 64 * e, tok0 + nk * CH);
+      }
+    }
+    ++nk;
+    k.next();
   };
-  if (!STATES) {
-    if (!wait_bar(x, B_FULL0, 0)) return;
-    scores(0);
+  auto load_x = [&]() {
+    if (leader) {
+      const uint32_t bar = x.bars + 8 * (B_XFULL + s.st), dst = x.sb + K::SM_X + s.st * K::X_BYTES;
+      expect_tx(bar, atoms * 8192);
+      tma_load_2d(dst, tx, bar, col, tok0 + nx * CH);
+      if (atoms == 2) tma_load_2d(dst + 8192, tx, bar, col + 64, tok0 + nx * CH);
+    }
+    ++nx;
+    s.next();
+  };
+#pragma unroll 1
+  while (nx < K::NX && nx < x.nchunks) {
+    if (nk < K::NB) load_k();
+    load_x();
   }
+#pragma unroll 1
   for (int i = 0; i < x.nchunks; ++i) {
-    const uint32_t xs = stage(i), b = xs + K::X_BYTES, c = b + K::KV_BYTES;
-    // U: the small terms first
-    if (!wait_bar(x, B_WX, i & 1)) return;
-    if (i > 0 && !wait_bar(x, B_UFREE, (i - 1) & 1)) return;
-    tc_fence_after();
-    {
-      const uint32_t id = idesc_bf16_f32(128, DK, 0, 1);
-#pragma unroll
-      for (int term = 2; term >= 0; --term)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_tmem_a(x.tmem + K::TM_U, x.tmem + K::TM_WX + term * 32 + k * 8, sdesc_sw128(b + k * 2048, 8192, 1024), id,
-                      term < 2 || k > 0);
-      umma_commit(&x.bars[B_U]);
-      if (STATES) umma_commit(&x.bars[B_EMPTY0 + i % NST]);
+    if (i + K::NB < x.nchunks) {  // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
+      if (!wait_bar(x, B_KFREE + k.st, k.ph ^ 1)) break;
+      load_k();
     }
-    if (STATES) continue;
-    if (i + 1 < x.nchunks) {
-      if (!wait_bar(x, B_FULL0 + (i + 1) % NST, ((i + 1) / NST) & 1)) return;
-      if (!wait_bar(x, B_GFREE, i & 1)) return;
+    if (!STATES) {
+      const int st = i % K::NX;
+      if (!wait_bar(x, B_YOUT + st, (i / K::NX) & 1)) break;
+      __syncwarp();
+      const int v = valid_rows(x, i);
+      const uint32_t at = K::SM_X + st * K::X_BYTES;
+      if (v == CH) {
+        if (leader) {
+          tma_store_2d(to, x.sb + at, col, tok0 + i * CH);
+          if (atoms == 2) tma_store_2d(to, x.sb + at + 8192, col + 64, tok0 + i * CH);
+          bulk_commit();
+          if (i + K::NX < x.nchunks) bulk_wait_read0();
+        }
+      } else {
+        __nv_bfloat16* out = (__nv_bfloat16*)t.a.out + col;
+#pragma unroll 1
+        for (int e = threadIdx.x & 31; e < atoms * v * 8; e += 32) {
+          const int atom = e / (v * 8), r = (e - atom * v * 8) >> 3, c = e & 7;
+          const uint4 u = *reinterpret_cast<const uint4*>(x.sm + at + atom * 8192 + r * 128 + ((c ^ (r & 7)) << 4));
+          *reinterpret_cast<uint4*>(out + ((int64_t)tok0 + i * CH + r) * ((int64_t)t.a.H * DV) + atom * 64 + c * 8) = u;
+        }
+      }
+    }
+    if (i + K::NX < x.nchunks) {
+      if (!wait_bar(x, B_XFREE + s.st, s.ph ^ 1)) break;
+      __syncwarp();
+      load_x();
+    }
+  }
+  // No copy stays in flight behind the block: the latest load of every stage, and every store.
+#pragma unroll 1
+  for (int i = 0; i < MAXST; ++i) {
+    const int cx = nx - 1 - i, ck = nk - 1 - i;
+    if (i < K::NX && cx >= 0) land(x.bars + 8 * (B_XFULL + cx % K::NX), (cx / K::NX) & 1);
+    if (i < K::NB && ck >= 0) land(x.bars + 8 * (B_KFULL + ck % K::NB), (ck / K::NB) & 1);
+  }
+  if (leader) bulk_wait_all();
+}
+
+// Two warps issue the products, U and the next chunk's G, and YI and YM (one
+// warp for all of them was the slowest role, and held YI back until the scores
+// had been made).  The whole warp walks the chunks, so that addresses stay
+// warp-uniform; one lane issues.
+template <int DK, int DV, bool STATES>
+__device__ __forceinline__ void role_mma_u(const Ctx& x, bool leader) {
+  using K = Cfg<DK, DV, STATES>;
+  constexpr uint32_t LBO = 8192 >> 4;  // between 64-column atoms
+  const uint32_t b0 = (x.sb + K::SM_K) >> 4;
+  Ring<K::NX> s, sn;  // this chunk's stages, and the next one's
+  Ring<K::NB> kr, kn;
+#pragma unroll 1
+  for (int i = STATES ? 0 : -1; i < x.nchunks; ++i) {
+    if (i >= 0) {
+      if (STATES && !wait_bar(x, B_KFULL + kr.st, kr.ph)) return;
+      if (i > 0 && !wait_bar(x, B_UFREE, (i - 1) & 1)) return;
+      uint32_t bb = (b0 + (uint32_t)kr.st * (K::K_BYTES >> 4)) | (LBO << 16), ta = x.tmem + K::TM_WX;
+      // by halves of the chunk, the small terms first
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half, bb += 256, ta += 64) {
+        if (!wait_bar(x, B_WX0 + half, i & 1)) return;
+        tc_fence_after();
+        if (leader) {
+          constexpr uint32_t id = idesc_bf16_f32(128, DK, 0, 1);
+#pragma unroll
+          for (int term = 3; term >= 0; --term) {
+            umma_ts_lo(x.tmem + K::TM_U, ta + 16 * term, bb, id, half > 0 || term < 3);
+            umma_ts_lo(x.tmem + K::TM_U, ta + 16 * term + 8, bb + 128, id, true);
+          }
+          commit(x, B_U0 + half);
+        }
+      }
+      if (leader) {
+        commit(x, B_KFREE + kr.st);
+        if (STATES) commit(x, B_XFREE + s.st);
+      }
+      s.next();
+      kr.next();
+    }
+    if (!STATES && i + 1 < x.nchunks) {
+      // the scalars as well, so that the scores' role has one wait for all
+      if (!wait_bar(x, B_KFULL + kn.st, kn.ph) || !wait_bar(x, B_DEC + sn.st, sn.ph)) return;
+      if (i >= 0 && !wait_bar(x, B_M0 + (i & 1), (i >> 1) & 1)) return;
       tc_fence_after();
-      scores(i + 1);
+      if (leader) {
+        constexpr uint32_t id = idesc_bf16_f32(64, 64, 0, 0);
+        const uint32_t bk = b0 + (uint32_t)kn.st * (K::K_BYTES >> 4), ck = bk + (K::KV >> 4);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint32_t o = (k >> 2) * LBO + (k & 3) * 2;
+          umma_ss_lo(x.tmem + K::TM_G, ck + o, bk + o, id, k > 0);
+        }
+        commit(x, B_G);
+      }
+      kn.next();
+      sn.next();
     }
+  }
+}
+
+template <int DK, int DV>
+__device__ __forceinline__ void role_mma_y(const Ctx& x, bool leader) {
+  using K = Cfg<DK, DV, false>;
+  constexpr uint32_t LBO = 8192 >> 4;
+  const uint32_t x0 = (x.sb + K::SM_X) >> 4, c0 = (x.sb + K::SM_K + K::KV) >> 4;
+  const uint32_t z0 = (x.sb + K::SM_Z0) >> 4, z1 = (x.sb + K::SM_Z1) >> 4, m0 = (x.sb + K::SM_M) >> 4;
+  const uint32_t tm = x.tmem;
+  const bool two = x.heads == 2;
+  Ring<K::NX> s;
+  Ring<K::NB> kr;
+#pragma unroll 1
+  for (int i = 0; i < x.nchunks; ++i, s.next(), kr.next()) {
+    if (!wait_bar(x, B_KFULL + kr.st, kr.ph)) return;
     if (!wait_bar(x, B_SRDY, i & 1)) return;
     if (i > 0 && !wait_bar(x, B_YFREE, (i - 1) & 1)) return;
     tc_fence_after();
-    {
-      const uint32_t id = idesc_bf16_f32(128, 64, 0, 0);
+    if (leader) {
+      constexpr uint32_t id = idesc_bf16_f32(128, 64, 0, 0);
+      const uint32_t ck = c0 + (uint32_t)kr.st * (K::K_BYTES >> 4);
 #pragma unroll
       for (int k = 0; k < DK / 16; ++k)
-        umma_tmem_a(x.tmem + K::TM_YI, x.tmem + K::TM_S + k * 8, sdesc_sw128(c + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024),
-                    id, k > 0);
-      umma_commit(&x.bars[B_SFREE]);
+        umma_ts_lo(tm + K::TM_YI, tm + K::TM_S + k * 8, ck + (k >> 2) * LBO + (k & 3) * 2, id, k > 0);
+      commit(x, B_SFREE);
+      commit(x, B_KFREE + kr.st);
     }
-    if (!wait_bar(x, B_M0 + (i & 1), (i >> 1) & 1)) return;
+    // (and x read by wx, since y goes over it once Y is there)
+    if (!wait_bar(x, B_M0 + (i & 1), (i >> 1) & 1) || !wait_bar(x, B_XREAD + s.st, s.ph)) return;
     tc_fence_after();
-    {
-      const uint32_t id = idesc_bf16_f32(128, 64, 1, 0);
-      const uint32_t m = x.sb + K::SM_M + (i & 1) * K::HEADS * K::M_BYTES;
+    if (leader) {
+      constexpr uint32_t id = idesc_bf16_f32(128, 64, 1, 0);
+      const uint32_t m = m0 + (i & 1) * (K::HEADS * K::M_BYTES >> 4), xs = x0 + s.st * (K::X_BYTES >> 4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         // x of head 0 and what stands below it: its other columns (dv = 128), the idle half, or zeros
-        const uint32_t xk = xs + k * 2048;
-        const uint32_t below = x.heads == 2 ? x.sb + K::SM_Z1 - xk : 8192u;
-        umma_ss(x.tmem + K::TM_YM, sdesc_sw128(xk, below, 1024), sdesc_sw128(m + k * 32, 16, 1024), id, k > 0);
+        const uint32_t xk = xs + k * 128, below = two ? z1 - xk : LBO;
+        umma_ss_lo(tm + K::TM_YM, xk | (below << 16), m + k * 2, id, k > 0);
       }
-      if (x.heads == 2) {
+      if (two) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t z = x.sb + K::SM_Z0, xk = xs + 8192 + k * 2048;
-          umma_ss(x.tmem + K::TM_YM, sdesc_sw128(z, xk - z, 1024), sdesc_sw128(m + K::M_BYTES + k * 32, 16, 1024), id, 1);
+          const uint32_t xk = xs + LBO + k * 128;
+          umma_ss_lo(tm + K::TM_YM, z0 | ((xk - z0) << 16), m + (K::M_BYTES >> 4) + k * 2, id, 1);
         }
       }
-      umma_commit(&x.bars[B_Y0 + (i & 1)]);
+      commit(x, B_Y0 + (i & 1));
     }
   }
 }
 
-// Decays and steps of every chunk; lane l takes tokens 2 l and 2 l + 1.
+// Decays and steps of every chunk.  delta comes three chunks ahead; the steps
+// are made 32 at a time (neighbours in memory: element e of a chunk is head
+// e % heads of token e / heads); then a half-warp takes a head, a lane 4 tokens
+// (with one head in the tile the upper half-warp repeats the lower one's).
 template <int DK, int DV, bool STATES>
 __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
-  using K = Cfg<DK, DV>;
+  using K = Cfg<DK, DV, STATES>;
+  constexpr int E = 2 * K::HEADS;  // elements per lane, at most
   const SsmArgs& a = t.a;
-  const int lane = threadIdx.x & 31;
-  float rate[K::HEADS], bias[K::HEADS], total[K::HEADS], raw[K::HEADS][2];
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const int h = x.heads == 2 ? lane >> 4 : 0;
+  const bool writes = (lane >> 4) == h;
+  const float rate = -expf(a.A_log[x.h0 + h]) * LOG2E;
+  const bool soft = a.dt_bias != nullptr;
+  float total = 0.f;
+  const int sh = x.heads - 1, per = 32 >> sh, tok = lane >> sh;  // tokens per 32 elements; this lane's first
+  const float bias = soft ? a.dt_bias[x.h0 + (lane & sh)] : 0.f;
+  const int64_t step = (int64_t)per * a.H;
+  const float* src = a.delta + (x.piece.start + tok) * a.H + x.h0 + (lane & sh);
+  int left = (int)(x.piece.end - x.piece.start) - tok;  // of the tokens from this lane's first one in the next fetch
+  uint32_t dst = 0;
+  const uint32_t raw0 = x.sb + K::SM_RAW + lane * 4;
+  auto fetch = [&]() {
+    const float* p = src;
 #pragma unroll
-  for (int h = 0; h < K::HEADS; ++h) {
-    const int hh = x.h0 + (h < x.heads ? h : 0);
-    rate[h] = -expf(a.A_log[hh]) * LOG2E;
-    bias[h] = a.dt_bias ? a.dt_bias[hh] : 0.f;
-    total[h] = 0.f;
-  }
-  auto fetch = [&](int i) {
-    const int v = valid_rows(x, i);
-#pragma unroll
-    for (int h = 0; h < K::HEADS; ++h)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        raw[h][k] = (h < x.heads && 2 * lane + k < v)
-                        ? a.delta[(x.piece.start + (int64_t)i * CH + 2 * lane + k) * a.H + x.h0 + h] : 0.f;
-  };
-  if (x.nchunks > 0) fetch(0);
-  for (int i = 0; i < x.nchunks; ++i) {
-    const int st = i % NST, v = valid_rows(x, i);
-    float cur[K::HEADS][2];
-#pragma unroll
-    for (int h = 0; h < K::HEADS; ++h) { cur[h][0] = raw[h][0]; cur[h][1] = raw[h][1]; }
-    if (i + 1 < x.nchunks) fetch(i + 1);
-    if (i >= NST && !__all_sync(0xffffffffu, wait_bar(x, B_EMPTY0 + st, (i / NST - 1) & 1))) return;
-#pragma unroll
-    for (int h = 0; h < K::HEADS; ++h) {
-      float* o = reinterpret_cast<float*>(x.sm + K::SM_DEC) + (st * K::HEADS + h) * SC_FLOATS;
-      float d[2], g[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        d[k] = a.dt_bias ? softplus_f32(cur[h][k] + bias[h]) : cur[h][k];
-        if (2 * lane + k >= v) d[k] = 0.f;
-        g[k] = rate[h] * d[k];
-      }
-      // sums up to each token, and from behind it to the chunk's end (each
-      // summed in its own direction: a weight near one has an exponent near zero)
-      float up = g[0] + g[1], down = up;
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, up, s), w = __shfl_down_sync(0xffffffffu, down, s);
-        if (lane >= s) up += u;
-        if (lane + s < 32) down += w;
-      }
-      float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
-      if (lane == 0) before = 0.f;
-      if (lane == 31) behind = 0.f;
-      const float c0 = before + g[0], c1 = up, r1 = behind, r0 = behind + g[1];
-      const float sum = __shfl_sync(0xffffffffu, up, 31);
-      total[h] += sum;
-      reinterpret_cast<float2*>(o + SC_W)[lane] = make_float2(ex2(r0) * d[0], ex2(r1) * d[1]);
-      if (lane == 0) reinterpret_cast<float*>(x.sm + K::SM_MISC + MS_TOTAL)[st * 2 + h] = ex2(sum);
-      if (!STATES) {
-        reinterpret_cast<float2*>(o + SC_CUM)[lane] = make_float2(c0, c1);
-        reinterpret_cast<float2*>(o + SC_D)[lane] = make_float2(d[0], d[1]);
-        reinterpret_cast<float2*>(o + SC_ECUM)[lane] = make_float2(ex2(c0), ex2(c1));
-        float mine = 0.f;
-#pragma unroll
-        for (int q = 1; q < 4; ++q) {
-          const float ref = __shfl_sync(0xffffffffu, up, 8 * q - 1);  // G before token 16 q
-          if (lane < 8 * q)
-            reinterpret_cast<float2*>(o + SC_ECD + 64 * (q - 1))[lane] = make_float2(ex2(ref - c0) * d[0], ex2(ref - c1) * d[1]);
-          if ((lane >> 3) == q) mine = ref;
-        }
-        reinterpret_cast<float2*>(o + SC_ER)[lane] = make_float2(ex2(c0 - mine), ex2(c1 - mine));
+    for (int k = 0; k < E; ++k, p += step) {
+      if (k * per < CH) {
+        const bool in = k * per < left;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(raw0 + dst + k * 128), "l"(in ? p : a.delta),
+                     "r"(in ? 4u : 0u)  // 0: zeros
+                     : "memory");
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    src += (int64_t)CH * a.H;
+    left -= CH;
+    dst = (dst + K::HEADS * CH * 4) & (4 * K::HEADS * CH * 4 - 1);
+  };
+  const float* raw = reinterpret_cast<const float*>(x.sm + K::SM_RAW) + lane;
+  float* put_d = reinterpret_cast<float*>(x.sm + K::SM_DEC) + (lane & sh) * K::SC_FLOATS + SC_D + tok;
+  float* out = reinterpret_cast<float*>(x.sm + K::SM_DEC) + h * K::SC_FLOATS + 4 * l;
+  Ring<K::NX> s;
+#pragma unroll 1
+  for (int i = x.nchunks > 0 ? -3 : 0; i < x.nchunks; ++i) {
+    __syncwarp();  // chunk i - 1's values have been read
+    fetch();       // chunk i + 3's
+    if (i < 0) continue;
+    const int v = valid_rows(x, i);
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
     __syncwarp();
-    if (lane == 0) mbar_arrive(&x.bars[B_DEC0 + st]);
+    float d[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) d[k] = raw[(i & 3) * K::HEADS * CH + 32 * k];
+    if (soft) {  // all of a lane's elements at once: one after the other they would hold the block up
+#pragma unroll
+      for (int k = 0; k < E; ++k) d[k] = softplus_f32(d[k] + bias);
+    }
+    if (i >= K::NX) {  // the slot's last readers: the state, and the outputs
+      wait_bar(x, B_XFREE + s.st, s.ph ^ 1);
+      if (!STATES) wait_bar(x, B_YOUT + s.st, s.ph ^ 1);
+    }
+    const int slot = s.st * (K::SC_SLOT / 4);
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k * per < CH) put_d[slot + k * per] = tok + k * per < v ? d[k] : 0.f;
+    __syncwarp();
+    float* o = out + slot;
+    const float4 d4 = *reinterpret_cast<const float4*>(o + SC_D);
+    const float g0 = rate * d4.x, g1 = rate * d4.y, g2 = rate * d4.z, g3 = rate * d4.w;
+    // sums up to each token, and from behind it to the chunk's end (each
+    // summed in its own direction: a weight near one has an exponent near zero)
+    const float c1 = g0 + g1, c2 = c1 + g2, c3 = c2 + g3, r1 = g3 + g2, r0 = r1 + g1;
+    float up = c3, down = r0 + g0;
+#pragma unroll
+    for (int e = 1; e < 16; e <<= 1) {
+      const float u = __shfl_up_sync(0xffffffffu, up, e, 16), w = __shfl_down_sync(0xffffffffu, down, e, 16);
+      if (l >= e) up += u;
+      if (l + e < 16) down += w;
+    }
+    const float sum = __shfl_sync(0xffffffffu, up, 15, 16);
+    float before = __shfl_up_sync(0xffffffffu, up, 1, 16), behind = __shfl_down_sync(0xffffffffu, down, 1, 16);
+    if (l == 0) before = 0.f;
+    if (l == 15) behind = 0.f;
+    total += sum;
+    if (writes) {
+      float2 w01 = make_float2(ex2(r0 + behind) * d4.x, ex2(r1 + behind) * d4.y);
+      float2 w23 = make_float2(ex2(g3 + behind) * d4.z, ex2(behind) * d4.w);
+      uint2* w = reinterpret_cast<uint2*>(o + SC_W - 2 * l);  // o is 4 l words in: two words per lane
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {  // by truncation: exact in three terms
+        w[16 * k] = make_uint2(upper_halves(w01), upper_halves(w23));
+        w01 = below_upper(w01);
+        w23 = below_upper(w23);
+      }
+      if (!STATES) {
+        const float4 cum = make_float4(before + g0, before + c1, before + c2, before + c3);
+        *reinterpret_cast<float4*>(o + SC_CUM) = cum;
+        *reinterpret_cast<float4*>(o + SC_LS) = make_float4(cum.x - __log2f(d4.x), cum.y - __log2f(d4.y),
+                                                            cum.z - __log2f(d4.z), cum.w - __log2f(d4.w));
+      }
+      if (l == 0) reinterpret_cast<float*>(x.sm + K::SM_MISC + MS_TOTAL)[s.st * 2 + h] = ex2(sum);
+    }
+    __syncwarp();
+    if (lane == 0) arrive(x, B_DEC + s.st);
+    s.next();
   }
-  if (STATES && lane == 0)
-    for (int h = 0; h < x.heads; ++h) t.piece_decay[(int64_t)(x.piece.slot0 + x.piece.r) * a.H + x.h0 + h] = total[h];
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (STATES && l == 0 && writes) t.piece_decay[(int64_t)(x.piece.slot0 + x.piece.r) * a.H + x.h0 + h] = total;
 }
 
-// w x, split into three bf16 terms, as the A operand of U.
-template <int DK, int DV>
+// w x as the A operand of U, in four bf16 terms.  With w = w1 + w2 + w3 (bf16
+// each), x w1 and x w2 have at most 16 bits, so that bf16 a = x w1 rounded and
+// x w1 - a by a fused multiply-add are exact together; the rest, x w3 and what
+// x w2 leaves, is 2^-16 of the whole and is rounded to 8 bits of it.  Five packed
+// instructions per two elements; a split of the fp32 product takes twelve.
+// By halves of the chunk: a half's terms are replaced as soon as its products
+// have read them.
+template <int DK, int DV, bool STATES>
 __device__ __forceinline__ void role_wx(const Ctx& x) {
-  using K = Cfg<DK, DV>;
+  using K = Cfg<DK, DV, STATES>;
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, tid = threadIdx.x - 32 * W_WX;
-  const uint32_t tl = x.tmem + ((uint32_t)(wq * 32) << 16);
-  bool ok = true;
-  for (int i = 0; i < x.nchunks; ++i) {
-    const int st = i % NST, v = valid_rows(x, i);
-    ok = ok && wait_bar(x, B_DEC0 + st, (i / NST) & 1);
-    ok = ok && wait_bar(x, B_FULL0 + st, (i / NST) & 1);
-    ok = ok && (i == 0 || wait_bar(x, B_U, (i - 1) & 1));
-    if (!named_sync_and(GRP_WX, 128, ok)) return;
-    tc_fence_after();
-    uint8_t* stg = x.sm + K::SM_STAGE + st * K::STAGE;
+  const uint32_t tl = x.tmem + ((uint32_t)(wq * 32) << 16) + K::TM_WX;
+  const int head = DV == 64 && wq >= 2 ? 1 : 0;
+  // this lane's row in 16 tokens and its 8-column chunk (tiles: columns 0-7, 8-15, then tokens 8-15)
+  const int row = ((lane >> 4) & 1) * 8 + (lane & 7), ch = (wq & 1) * 4 + ((lane >> 3) & 1);
+  const uint32_t xl = x.sb + K::SM_X + (wq >> 1) * 8192 + row * 128;
+  const uint32_t sw0 = (uint32_t)(ch ^ (row & 7)) << 4, sw1 = (uint32_t)((ch + 2) ^ (row & 7)) << 4;
+  Ring<K::NX> s;
+  Ring<K::NB> kr;
+#pragma unroll 1
+  for (int i = 0; i < x.nchunks; ++i, s.next(), kr.next()) {
+    wait_bar(x, B_DEC + s.st, s.ph);
+    wait_bar(x, B_XFULL + s.st, s.ph);
+    const int v = valid_rows(x, i);
     if (v < CH) {
       // Rows behind the sequence's end hold other data: x and b become zero,
       // so that nothing of them (an infinity among it) reaches a product.
+      wait_bar(x, B_KFULL + kr.st, kr.ph);
       constexpr int ATOMS = 2 + DK / 64;
+#pragma unroll 1
       for (int e = tid; e < ATOMS * (CH - v) * 8; e += 128) {
         const int atom = e / ((CH - v) * 8), k = e - atom * (CH - v) * 8;
-        *reinterpret_cast<uint4*>(stg + atom * 8192 + v * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+        uint8_t* at = x.sm + (atom < 2 ? K::SM_X + s.st * K::X_BYTES + atom * 8192
+                                       : K::SM_K + kr.st * K::K_BYTES + (atom - 2) * 8192);
+        *reinterpret_cast<uint4*>(at + v * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
       named_sync(GRP_WX, 128);
     }
-    const int head = DV == 64 && wq >= 2 ? 1 : 0;
-    const float* w = reinterpret_cast<const float*>(x.sm + K::SM_DEC) + (st * K::HEADS + head) * SC_FLOATS + SC_W;
-    const uint32_t xa = smem_u32(stg) + (wq >> 1) * 8192;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + head * K::SC_FLOATS + SC_W + (lane & 3);
+    uint32_t xa = xl + s.st * K::X_BYTES;
+#pragma unroll 1
+    for (int tb = 0; tb < 2; ++tb, w += 16, xa += 4096) {  // 32 tokens
+      uint32_t w1[4], w2[4], w3[4];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {      // 16 columns of the warp's 32
-      const int pc = (wq & 1) * 4 + half * 2;   // their first 8-column chunk in the atom
+      for (int k = 0; k < 4; ++k) {
+        w1[k] = w[4 * k];
+        w2[k] = w[32 + 4 * k];
+        w3[k] = w[64 + 4 * k];
+      }
+      if (i > 0) wait_bar(x, B_U0 + tb, (i - 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {  // 16 columns of the warp's 32
+        uint32_t a1[8], e1[8], a2[8], lo[8];
+        const uint32_t xe = xa + (half ? sw1 : sw0);
 #pragma unroll
-      for (int tb = 0; tb < 2; ++tb) {          // 32 tokens
-        uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {           // 16 tokens: tiles (columns 0-7, 8-15) x (tokens 0-7, 8-15)
-          const int t0 = 32 * tb + 16 * k;
-          const int row = t0 + ((lane >> 4) & 1) * 8 + (lane & 7), ch = pc + ((lane >> 3) & 1);
+        for (int k = 0; k < 2; ++k) {
           uint32_t raw[4];
-          ldsm_x4_t(xa + row * 128 + ((ch ^ (row & 7)) << 4), raw);
+          ldsm_x4_t(xe + k * 2048, raw);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 wt = *reinterpret_cast<const float2*>(w + t0 + (j >> 1) * 8 + 2 * (lane & 3));
-            float2 val = __fmul2_rn(bf16x2_f32(raw[j]), wt);
-            hi[4 * k + j] = upper_halves(val);
-            val = minus_upper(val);
-            mid[4 * k + j] = upper_halves(val);
-            val = minus_upper(val);
-            lo[4 * k + j] = upper_halves(val);
+            const int o = 4 * k + j, m = 2 * k + (j >> 1);
+            a1[o] = mul_bf16x2(raw[j], w1[m]);
+            e1[o] = fms_bf16x2(raw[j], w1[m], a1[o]);
+            a2[o] = mul_bf16x2(raw[j], w2[m]);
+            lo[o] = fma_bf16x2(raw[j], w3[m], fms_bf16x2(raw[j], w2[m], a2[o]));
           }
         }
-        const uint32_t ta = tl + ((uint32_t)(half * 16) << 16) + K::TM_WX + tb * 16;
-        tmem_st_16x128b_x4(ta, hi);
-        tmem_st_16x128b_x4(ta + 32, mid);
-        tmem_st_16x128b_x4(ta + 64, lo);
+        const uint32_t ta = tl + ((uint32_t)(half * 16) << 16) + tb * 64;
+        tmem_st_16x128b_x4(ta, a1);
+        tmem_st_16x128b_x4(ta + 16, e1);
+        tmem_st_16x128b_x4(ta + 32, a2);
+        tmem_st_16x128b_x4(ta + 48, lo);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(x, B_WX0 + tb);
+      if (!STATES && tb) arrive(x, B_XREAD + s.st);  // the outputs may go over x
     }
-    tmem_wait_st();
-    tc_fence_before();
-    mbar_arrive(&x.bars[B_WX]);
   }
 }
 
-// G to M: decay, step and causal mask, bf16, as the B operand of YM.  Warp q
-// has tokens 16 q .. 16 q + 15; tiles above the diagonal stay zero.
+// Eight warps turn G into M and combine the outputs, a chunk apart: the scores
+// of chunk j + 1 are made before the outputs of chunk j, whose products run
+// meanwhile.
+//   Scores: decay, step and causal mask, bf16, as the B operand of YM.  Warps q
+// and q + 4 have tokens 16 q .. 16 q + 15, a head each (dv = 64) or 32 columns
+// each; what lies above the diagonal is zero.
+//   Outputs: y = e^{G_t} YI + YM + D x, over x's own tile.  Warps q and q + 4
+// have value columns 32 q .. 32 q + 31, half the tokens each.
 template <int DK, int DV>
-__device__ __forceinline__ void role_scores(const Ctx& x) {
-  using K = Cfg<DK, DV>;
-  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
-  const uint32_t tl = x.tmem + ((uint32_t)(q * 32) << 16) + K::TM_G;
+__device__ __forceinline__ void role_scores_out(const Ctx& x, const TcArgs& t) {
+  using K = Cfg<DK, DV, false>;
+  const SsmArgs& a = t.a;
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, tid = threadIdx.x - 32 * W_SO, second = tid >> 7;
+  const uint32_t tl = x.tmem + ((uint32_t)(q * 32) << 16);
+  // scores: this thread's rows r0, r0 + 8 and columns cl, cl + 1 (+ 8); its row address
+  // in a 16x16 tile (four 8x8 matrices: rows 0-7, rows 8-15, then columns 8-15)
   const int r0 = 16 * q + (lane >> 2), cl = 2 * (lane & 3);
-  // this lane's row address in a 16x16 tile (four 8x8 matrices: rows 0-7, rows 8-15, then columns 8-15)
   const int srow = 16 * q + ((lane >> 3) & 1) * 8 + (lane & 7), sch = (lane >> 4) & 1;
-  bool ok = true;
-  for (int i = 0; i < x.nchunks; ++i) {
-    const int st = i % NST;
-    ok = ok && wait_bar(x, B_DEC0 + st, (i / NST) & 1);
-    ok = ok && (i < 2 || wait_bar(x, B_Y0 + (i & 1), ((i >> 1) - 1) & 1));
-    ok = ok && wait_bar(x, B_G, i & 1);
-    if (!named_sync_and(GRP_SC, 128, ok)) return;
-    tc_fence_after();
-    float g[4][8];
-    {
-      float ga[16], gb[16];
+  const bool by_head = x.heads == 2;
+  const int sc_off = by_head ? second * K::SC_FLOATS : 0, j_first = by_head ? 0 : second, j_step = by_head ? 1 : 2;
+  const uint32_t ml = x.sb + K::SM_M + srow * 128 + (by_head ? second * K::M_BYTES : 0);
+  // bits of the pairs (row r0 + 8 (k % 2), columns 8 (k / 2) + cl and the next) that
+  // lie on or below the diagonal, in the 32 columns that it crosses
+  uint32_t keep[8];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) ga[k] = gb[k] = 0.f;
-      tmem_ld_16x256b_x2(tl, ga);
-      if (q >= 1) tmem_ld_16x256b_x2(tl + 16, ga + 8);
-      if (q >= 2) tmem_ld_16x256b_x2(tl + 32, gb);
-      if (q >= 3) tmem_ld_16x256b_x2(tl + 48, gb + 8);
-      tmem_wait_ld(ga);
-      tmem_wait_ld(gb);
+  for (int k = 0; k < 8; ++k) {
+    const int below = r0 + 8 * (k & 1) - (32 * (q >> 1) + 8 * (k >> 1) + cl);
+    keep[k] = below > 0 ? 0xffffffffu : (below == 0 ? 0xffffu : 0u);
+  }
+  // outputs
+  const int hl = DV == 64 && q >= 2 ? 1 : 0;
+  const float skip = a.D ? a.D[x.h0 + (hl < x.heads ? hl : 0)] : 0.f;
+  const float2 skip2 = make_float2(skip, skip);
+  const int row = ((lane >> 4) & 1) * 8 + (lane & 7), ch = (q & 1) * 4 + ((lane >> 3) & 1);
+  const uint32_t xl = x.sb + K::SM_X + (q >> 1) * 8192 + row * 128 + second * 4096;
+  const uint32_t sw0 = (uint32_t)(ch ^ (row & 7)) << 4, sw1 = (uint32_t)((ch + 2) ^ (row & 7)) << 4;
+  Ring<K::NX> s, so;  // stages of the scores' chunk and of the outputs'
+#pragma unroll 1
+  for (int i = 0; i <= x.nchunks; ++i) {
+    if (i < x.nchunks) {
+      wait_bar(x, B_G, i & 1);  // (M's buffer is free: this thread has waited for Y of chunk i - 2)
+      __syncwarp();
+      tc_fence_after();
+      const float* sc = reinterpret_cast<const float*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + sc_off;
+      const uint32_t mb = ml + (i & 1) * K::HEADS * K::M_BYTES;
+      const float2 c00 = make_float2(sc[SC_CUM + r0], sc[SC_CUM + r0]), c11 = make_float2(sc[SC_CUM + r0 + 8], sc[SC_CUM + r0 + 8]);
+#pragma unroll 1
+      for (int j = j_first; j <= q >> 1; j += j_step) {  // 32 columns at a time, so that their chains overlap
+        float g[16];
+        tmem_ld_16x256b_x4_wait(tl + K::TM_G + 32 * j, g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) { g[0][k] = ga[k]; g[1][k] = ga[8 + k]; g[2][k] = gb[k]; g[3][k] = gb[8 + k]; }
-    }
-    tc_fence_before();
-    mbar_arrive(&x.bars[B_GFREE]);
-    const uint32_t mb = x.sb + K::SM_M + (i & 1) * K::HEADS * K::M_BYTES;
-#pragma unroll
-    for (int h = 0; h < K::HEADS; ++h) {
-      if (h >= x.heads) break;
-      const float* s = reinterpret_cast<const float*>(x.sm + K::SM_DEC) + (st * K::HEADS + h) * SC_FLOATS;
-      const uint32_t mh = mb + h * K::M_BYTES + srow * 128;
-      const float er0 = s[SC_ER + r0], er1 = s[SC_ER + r0 + 8];
-      const float c0 = s[SC_CUM + r0], c1 = s[SC_CUM + r0 + 8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > q) break;
-        float m[8];
-        if (j < q) {  // the whole tile lies before the rows: two factors, none above one
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 e = *reinterpret_cast<const float2*>(s + SC_ECD + 64 * (q - 1) + 16 * j + 8 * k + cl);
-            m[4 * k] = g[j][4 * k] * er0 * e.x;
-            m[4 * k + 1] = g[j][4 * k + 1] * er0 * e.y;
-            m[4 * k + 2] = g[j][4 * k + 2] * er1 * e.x;
-            m[4 * k + 3] = g[j][4 * k + 3] * er1 * e.y;
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int sc = 16 * q + 8 * k + cl;
-            const float2 cs = *reinterpret_cast<const float2*>(s + SC_CUM + sc), ds = *reinterpret_cast<const float2*>(s + SC_D + sc);
-            m[4 * k] = sc <= r0 ? g[j][4 * k] * ex2(c0 - cs.x) * ds.x : 0.f;
-            m[4 * k + 1] = sc + 1 <= r0 ? g[j][4 * k + 1] * ex2(c0 - cs.y) * ds.y : 0.f;
-            m[4 * k + 2] = sc <= r0 + 8 ? g[j][4 * k + 2] * ex2(c1 - cs.x) * ds.x : 0.f;
-            m[4 * k + 3] = sc + 1 <= r0 + 8 ? g[j][4 * k + 3] * ex2(c1 - cs.y) * ds.y : 0.f;
-          }
+        for (int k = 0; k < 4; ++k) {  // columns 32 j + 8 k + cl, and the next
+          const float2 ls = *reinterpret_cast<const float2*>(sc + SC_LS + 32 * j + 8 * k + cl);
+          const float2 nls = make_float2(-ls.x, -ls.y);
+          const float2 a0 = __fadd2_rn(c00, nls), a1 = __fadd2_rn(c11, nls);
+          const float2 m0 = __fmul2_rn(make_float2(g[4 * k], g[4 * k + 1]), make_float2(ex2(a0.x), ex2(a0.y)));
+          const float2 m1 = __fmul2_rn(make_float2(g[4 * k + 2], g[4 * k + 3]), make_float2(ex2(a1.x), ex2(a1.y)));
+          g[4 * k] = m0.x;
+          g[4 * k + 1] = m0.y;
+          g[4 * k + 2] = m1.x;
+          g[4 * k + 3] = m1.y;
         }
-        const uint32_t pk[4] = {pack_bf16x2(m[0], m[1]), pack_bf16x2(m[2], m[3]), pack_bf16x2(m[4], m[5]),
-                                pack_bf16x2(m[6], m[7])};
-        stsm_x4(mh + (((2 * j + sch) ^ (srow & 7)) << 4), pk);
+        uint32_t pk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(g[2 * k], g[2 * k + 1]);
+        if (j == q >> 1) {  // cut out, not multiplied: what stands above the diagonal may be anything
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pk[k] &= keep[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t t4[4] = {pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]};
+          stsm_x4(mb + (((4 * j + 2 * k + sch) ^ (srow & 7)) << 4), t4);
+        }
       }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      arrive(x, B_M0 + (i & 1));  // G may be overwritten, M is there
+      s.next();
     }
-    fence_proxy_async_smem();
-    mbar_arrive(&x.bars[B_M0 + (i & 1)]);
+    if (i > 0) {
+      const int o = i - 1;
+      wait_bar(x, B_Y0 + (o & 1), (o >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      const float* ec = reinterpret_cast<const float*>(x.sm + K::SM_DEC + so.st * K::SC_SLOT) + hl * K::SC_FLOATS + SC_CUM + cl + 32 * second;
+      const uint32_t xa = xl + so.st * K::X_BYTES;
+      float2 f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 c = *reinterpret_cast<const float2*>(ec + 8 * k);
+        f[k] = make_float2(ex2(c.x), ex2(c.y));
+      }
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {  // 16 columns of the warp's 32
+        float yi[16], ym[16];
+        const uint32_t te = tl + K::TM_YI + 32 * second + ((uint32_t)(half * 16) << 16), xe = xa + (half ? sw1 : sw0);
+        tmem_ld_16x256b_x4x2_wait(te, te + (K::TM_YM - K::TM_YI), yi, ym);
+        if (half) {
+          tc_fence_before();
+          arrive(x, B_YFREE);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t raw[4], pk[4];
+          ldsm_x4_t(xe + k * 2048, raw);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 8 * k + 2 * j;
+            float2 y = __ffma2_rn(f[2 * k + (j >> 1)], make_float2(yi[e], yi[e + 1]), make_float2(ym[e], ym[e + 1]));
+            y = __ffma2_rn(skip2, bf16x2_f32(raw[j]), y);
+            pk[j] = pack_bf16x2(y.x, y.y);
+          }
+          stsm_x4_t(xe + k * 2048, pk);
+        }
+      }
+      fence_proxy_async_smem();
+      arrive(x, B_YOUT + so.st);
+      so.next();
+    }
   }
 }
 
-// S in registers: thread (lane p, half of the key channels).
+// S in registers: thread (lane p, a quarter of the key channels).  Sixteen warps,
+// so that U is free again soon: the next chunk's product waits for it.
 template <int DK, int DV, bool STATES>
 __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
-  using K = Cfg<DK, DV>;
-  constexpr int NC = DK / 2;
+  using K = Cfg<DK, DV, STATES>;
+  constexpr int NC = DK * 4 / ST_WARPS;
   const SsmArgs& a = t.a;
   const int w = (threadIdx.x >> 5) - W_ST, lane = threadIdx.x & 31, p = (w & 3) * 32 + lane, n0 = (w >> 2) * NC;
   const uint32_t tl = x.tmem + ((uint32_t)((w & 3) * 32) << 16);
@@ -634,6 +931,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
 #pragma unroll
       for (int n = 0; n < NC; ++n) S[n] = slots[s0 * seq + (int64_t)n * DV];
     }
+#pragma unroll 1
     for (int r = 0; r < x.piece.r; ++r) {
       const float dec = ex2(t.piece_decay[(s0 + r) * a.H + x.h0 + head]);
       const float* o = slots + (s0 + r + 1) * seq;
@@ -652,47 +950,47 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
       }
     }
   }
-  auto publish = [&]() {  // S as bf16 pairs: the A operand of YI
+  const float* totals = reinterpret_cast<const float*>(x.sm + K::SM_MISC + MS_TOTAL) + head;
+  Ring<K::NX> s;
+#pragma unroll 1
+  for (int i = 0; i < x.nchunks; ++i, s.next()) {
+    if (!STATES) {  // S before the chunk as bf16 pairs: the A operand of YI
+      if (i > 0) wait_bar(x, B_SFREE, (i - 1) & 1);
+      __syncwarp();
+      tc_fence_after();
 #pragma unroll
-    for (int k = 0; k < NC / 16; ++k) {
-      uint32_t pk[8];
+      for (int k = 0; k < NC / 16; ++k) {
+        uint32_t pk[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(S[16 * k + 2 * j], S[16 * k + 2 * j + 1]);
-      tmem_st8(tl + K::TM_S + (n0 >> 1) + 8 * k, pk);
+        for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(S[16 * k + 2 * j], S[16 * k + 2 * j + 1]);
+        tmem_st8(tl + K::TM_S + (n0 >> 1) + 8 * k, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(x, B_SRDY);
     }
-    tmem_wait_st();
-    tc_fence_before();
-    mbar_arrive(&x.bars[B_SRDY]);
-  };
-  __syncwarp();
-  if (!STATES && x.nchunks > 0) publish();
-  bool ok = true;
-  for (int i = 0; i < x.nchunks; ++i) {
-    const int st = i % NST;
-    ok = ok && wait_bar(x, B_DEC0 + st, (i / NST) & 1);
-    ok = ok && wait_bar(x, B_U, i & 1);
-    if (!named_sync_and(GRP_ST, 256, ok)) return;
+    wait_bar(x, B_U1, i & 1);  // (made from this chunk's scalars)
+    __syncwarp();
     tc_fence_after();
-    const float dec = reinterpret_cast<const float*>(x.sm + K::SM_MISC + MS_TOTAL)[st * 2 + head];
+    const float dec = totals[s.st * 2];
+    const float2 dec2 = make_float2(dec, dec);
 #pragma unroll
     for (int k = 0; k < NC / 16; ++k) {
       float u[16];
       tmem_ld16(tl + K::TM_U + n0 + 16 * k, u);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) S[16 * k + j] = fmaf(S[16 * k + j], dec, u[j]);
+      for (int j = 0; j < 16; j += 2) {
+        const float2 v = __ffma2_rn(make_float2(S[16 * k + j], S[16 * k + j + 1]), dec2, make_float2(u[j], u[j + 1]));
+        S[16 * k + j] = v.x;
+        S[16 * k + j + 1] = v.y;
+      }
     }
     tc_fence_before();
-    mbar_arrive(&x.bars[B_UFREE]);
+    arrive(x, B_UFREE);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&x.bars[B_EMPTY0 + st]);
-    if (!STATES && i + 1 < x.nchunks) {
-      ok = wait_bar(x, B_SFREE, i & 1);
-      __syncwarp();
-      tc_fence_after();
-      publish();
-    }
+    if (lane == 0) arrive(x, B_XFREE + s.st);
   }
-  if (!live || !ok) return;
+  if (!live) return;
   float* o = nullptr;
   if (STATES)
     o = slots + (int64_t)(x.piece.slot0 + x.piece.r + 1) * seq;
@@ -704,84 +1002,12 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
   }
 }
 
-// y = e^{G_t} YI + YM + D x, over x's own tile, then out by TMA (a chunk cut
-// short by the sequence's end: row by row).
-template <int DK, int DV>
-__device__ __forceinline__ void role_out(const Ctx& x, const TcArgs& t, const void* to) {
-  using K = Cfg<DK, DV>;
-  const SsmArgs& a = t.a;
-  const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, tid = threadIdx.x - 32 * W_OUT;
-  const uint32_t tl = x.tmem + ((uint32_t)(wq * 32) << 16);
-  const int hl = DV == 64 && wq >= 2 ? 1 : 0;
-  const float skip = a.D ? a.D[x.h0 + (hl < x.heads ? hl : 0)] : 0.f;
-  const float2 skip2 = make_float2(skip, skip);
-  const int atoms = x.heads * DV / 64;
-  bool ok = true;
-  for (int i = 0; i < x.nchunks; ++i) {
-    const int st = i % NST, v = valid_rows(x, i);
-    ok = ok && wait_bar(x, B_DEC0 + st, (i / NST) & 1);
-    ok = ok && wait_bar(x, B_FULL0 + st, (i / NST) & 1);
-    ok = ok && wait_bar(x, B_Y0 + (i & 1), (i >> 1) & 1);
-    if (!named_sync_and(GRP_OUT, 128, ok)) break;
-    tc_fence_after();
-    uint8_t* stg = x.sm + K::SM_STAGE + st * K::STAGE;
-    const float* ec = reinterpret_cast<const float*>(x.sm + K::SM_DEC) + (st * K::HEADS + hl) * SC_FLOATS + SC_ECUM;
-    const uint32_t xa = smem_u32(stg) + (wq >> 1) * 8192;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int pc = (wq & 1) * 4 + half * 2;
-      const uint32_t ta = tl + ((uint32_t)(half * 16) << 16);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {  // 16 tokens
-        float yi[16], *ym = yi + 8;
-        tmem_ld_16x256b_x2(ta + K::TM_YI + 16 * tb, yi);
-        tmem_ld_16x256b_x2(ta + K::TM_YM + 16 * tb, ym);
-        const int row = 16 * tb + ((lane >> 4) & 1) * 8 + (lane & 7), ch = pc + ((lane >> 3) & 1);
-        const uint32_t xaddr = xa + row * 128 + ((ch ^ (row & 7)) << 4);
-        uint32_t raw[4];
-        ldsm_x4_t(xaddr, raw);
-        tmem_wait_ld(yi);
-        uint32_t pk[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 e = *reinterpret_cast<const float2*>(ec + 16 * tb + (j >> 1) * 8 + 2 * (lane & 3));
-          float2 y = __ffma2_rn(e, make_float2(yi[2 * j], yi[2 * j + 1]), make_float2(ym[2 * j], ym[2 * j + 1]));
-          y = __ffma2_rn(skip2, bf16x2_f32(raw[j]), y);
-          pk[j] = pack_bf16x2(y.x, y.y);
-        }
-        stsm_x4_t(xaddr, pk);
-      }
-    }
-    tc_fence_before();
-    mbar_arrive(&x.bars[B_YFREE]);
-    fence_proxy_async_smem();
-    named_sync(GRP_OUT, 128);
-    const int64_t tok = x.piece.start + (int64_t)i * CH;
-    if (v == CH) {
-      if (tid == 0) {
-        for (int k = 0; k < atoms; ++k) tma_store_2d(to, smem_u32(stg) + k * 8192, x.h0 * DV + 64 * k, (int)tok);
-        bulk_commit();
-        bulk_wait_read0();
-        mbar_arrive(&x.bars[B_EMPTY0 + st]);
-      }
-    } else {  // only a piece's last chunk
-      __nv_bfloat16* out = (__nv_bfloat16*)a.out + (int64_t)x.h0 * DV;
-      for (int e = tid; e < atoms * v * 8; e += 128) {
-        const int atom = e / (v * 8), row = (e - atom * v * 8) >> 3, c = e & 7;
-        const uint4 u = *reinterpret_cast<const uint4*>(stg + atom * 8192 + row * 128 + ((c ^ (row & 7)) << 4));
-        *reinterpret_cast<uint4*>(out + (tok + row) * ((int64_t)a.H * DV) + atom * 64 + c * 8) = u;
-      }
-    }
-  }
-  if (tid == 0) bulk_wait_all();
-}
-
 template <int DK, int DV, bool STATES>
 __global__ void __launch_bounds__(NTHR, 1)
     ssm_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
                   const __grid_constant__ CUtensorMap tc, const __grid_constant__ CUtensorMap to,
                   const __grid_constant__ TcArgs t) {
-  using K = Cfg<DK, DV>;
+  using K = Cfg<DK, DV, STATES>;
   extern __shared__ uint8_t smem_raw[];
   Ctx x;
   x.tile = blockIdx.x % t.tiles;
@@ -789,23 +1015,24 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (STATES && x.piece.r == x.piece.pieces - 1) return;  // nothing follows it
   x.sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   x.sb = smem_u32(x.sm);
-  x.bars = reinterpret_cast<uint64_t*>(x.sm + K::SM_MISC);
-  x.abort = reinterpret_cast<volatile int*>(x.sm + K::SM_MISC + MS_ABORT);
-  x.status = t.a.status;
+  x.bars = x.sb + K::SM_MISC;
   x.heads = t.hpt;
   x.h0 = x.tile * t.hpt;
-  x.nchunks = (int)((x.piece.end - x.piece.start + CH - 1) / CH);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < NUM_BARS; ++i) {
-      int n = 1;
-      if (i >= B_EMPTY0 && i < B_EMPTY0 + NST) n = 1 + 8;
-      if (i == B_WX || i == B_GFREE || i == B_M0 || i == B_M1 || i == B_YFREE) n = 128;
-      if (i == B_UFREE || i == B_SRDY) n = 256;
-      mbar_init(&x.bars[i], n);
-    }
+  x.nchunks = ((int)(x.piece.end - x.piece.start) + CH - 1) / CH;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  uint8_t* misc = x.sm + K::SM_MISC;
+  if (tid < NUM_BARS) {
+    int n = 1;
+    if (tid >= B_XFREE && tid < B_XFREE + MAXST) n = STATES ? ST_WARPS + 1 : ST_WARPS;
+    if (!STATES && ((tid >= B_KFREE && tid < B_KFREE + MAXST) || tid == B_DRAIN)) n = 2;
+    if (tid == B_WX0 || tid == B_WX1 || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = 128;
+    if (tid == B_UFREE || tid == B_SRDY) n = 32 * ST_WARPS;
+    if (tid == B_M0 || tid == B_M1 || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = 256;
+    mbar_init(reinterpret_cast<uint64_t*>(misc) + tid, n);
     fence_mbar_init();
-    *x.abort = 0;
+  }
+  if (tid == 0) {
+    *reinterpret_cast<volatile int*>(misc + MS_ABORT) = 0;
     prefetch_tmap(&tx);
     prefetch_tmap(&tb);
     prefetch_tmap(&tc);
@@ -821,36 +1048,38 @@ __global__ void __launch_bounds__(NTHR, 1)
     fence_proxy_async_smem();
   }
   if (warp == 0) {
-    tmem_alloc(reinterpret_cast<uint32_t*>(x.sm + K::SM_MISC + MS_TMEM), K::TM_COLS);
+    tmem_alloc(reinterpret_cast<uint32_t*>(misc + MS_TMEM), K::TM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  x.tmem = *reinterpret_cast<volatile uint32_t*>(x.sm + K::SM_MISC + MS_TMEM);
+  x.tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(misc + MS_TMEM), 0);
 
-  if (warp == W_TMA) {
-    if (lane == 0) role_load<DK, DV, STATES>(x, &tx, &tb, &tc, x.h0 / (t.a.H / t.a.G));
-  } else if (warp == W_MMA) {
-    if (lane == 0) {
-      if (x.nchunks > 0) role_mma<DK, DV, STATES>(x);
-      umma_commit(&x.bars[B_DRAIN]);  // every product has ended before TMEM is released
-      mbar_wait(&x.bars[B_DRAIN], 0, WAIT_NS);
+  if (warp >= W_MOVE) {
+    if (warp == W_MOVE) {
+      role_move<DK, DV, STATES>(x, t, &tx, &tb, &tc, &to, elect_one());
+    } else if (warp == W_DEC) {
+      role_decay<DK, DV, STATES>(x, t);
+    } else if (!STATES || warp == W_MMU) {
+      const bool leader = elect_one();
+      if (warp == W_MMU) role_mma_u<DK, DV, STATES>(x, leader);
+      else if (!STATES) role_mma_y<DK, DV>(x, leader);
+      __syncwarp();
+      if (leader) commit(x, B_DRAIN);  // every product has ended before TMEM is released
+      land(x.bars + 8 * B_DRAIN, 0);
     }
-  } else if (warp == W_DEC) {
-    role_decay<DK, DV, STATES>(x, t);
   } else if (warp >= W_ST) {
     role_state<DK, DV, STATES>(x, t);
-  } else if (warp >= W_OUT) {
-    if (!STATES) role_out<DK, DV>(x, t, &to);
-  } else if (warp >= W_SC) {
-    if (!STATES) role_scores<DK, DV>(x);
+  } else if (warp >= W_SO) {
+    if (!STATES) role_scores_out<DK, DV>(x, t);
   } else {
-    role_wx<DK, DV>(x);
+    role_wx<DK, DV, STATES>(x);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *reinterpret_cast<volatile int*>(misc + MS_ABORT) != 0) record_error(t.a.status, KDA_ERR_TIMEOUT, 1);
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(x.tmem, K::TM_COLS);
@@ -949,9 +1178,14 @@ Plan make_plan(int N, int64_t T, int H, int G, int dk, int dv, bool packed) {
   return p;
 }
 
+template <int DK, int DV, bool STATES>
+cudaError_t ready() {
+  return cudaFuncSetAttribute(ssm_tc_kernel<DK, DV, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Cfg<DK, DV, STATES>::BYTES);
+}
+
 template <int DK, int DV>
 cudaError_t launch(const TcArgs& t, const Plan& p, cudaStream_t s) {
-  using K = Cfg<DK, DV>;
   const SsmArgs& a = t.a;
   const int64_t rows = a.cu ? a.T : (int64_t)a.N * a.T;
   CUtensorMap tx, tb, tc, to;
@@ -966,13 +1200,11 @@ cudaError_t launch(const TcArgs& t, const Plan& p, cudaStream_t s) {
   }
   cudaError_t e;
   if (p.split) {
-    auto* k1 = ssm_tc_kernel<DK, DV, true>;
-    if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::BYTES)) != cudaSuccess) return e;
-    k1<<<blocks, NTHR, K::BYTES, s>>>(tx, tb, tc, to, t);
+    if ((e = ready<DK, DV, true>()) != cudaSuccess) return e;
+    ssm_tc_kernel<DK, DV, true><<<blocks, NTHR, Cfg<DK, DV, true>::BYTES, s>>>(tx, tb, tc, to, t);
   }
-  auto* k2 = ssm_tc_kernel<DK, DV, false>;
-  if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::BYTES)) != cudaSuccess) return e;
-  k2<<<blocks, NTHR, K::BYTES, s>>>(tx, tb, tc, to, t);
+  if ((e = ready<DK, DV, false>()) != cudaSuccess) return e;
+  ssm_tc_kernel<DK, DV, false><<<blocks, NTHR, Cfg<DK, DV, false>::BYTES, s>>>(tx, tb, tc, to, t);
   return cudaGetLastError();
 }
 
