@@ -28,9 +28,9 @@
 // bf16 itself, and the three are of one size.
 //
 // Roles (32 warps, one block per SM): wx (4 warps) weights x and stores its
-// terms; scores and outputs (8) turn G into M and combine YI, YM and the skip
-// over x's own tile; state (16) holds S; one warp each for the copies, the
-// issue of U, that of the other products, and the chunk's scalars.
+// terms; scores (8) turn G into M; state (16) holds S and combines YI, YM and
+// the skip over x's own tile; one warp each for the copies, the issue of U and
+// G, that of YI and YM, and the chunk's scalars.
 //
 // Pieces.  A sequence longer than the plan's piece length is cut into pieces
 // that run in parallel: a first pass (states only) gives each piece's own state
@@ -49,10 +49,11 @@ constexpr int PT = 128;      // value columns per tile
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // limit of every in-kernel wait
 
-constexpr int W_WX = 0, W_SO = 4, W_ST = 12, ST_WARPS = 16, W_MOVE = W_ST + ST_WARPS, W_MMY = W_MOVE + 1, W_MMU = W_MOVE + 2, W_DEC = W_MOVE + 3,
+constexpr int W_WX = 0, W_SC = 4, W_ST = 12, ST_WARPS = 16, W_MOVE = W_ST + ST_WARPS, W_MMY = W_MOVE + 1, W_MMU = W_MOVE + 2, W_DEC = W_MOVE + 3,
               NWARP = W_MOVE + 4;
 constexpr int NTHR = 32 * NWARP;
 enum { GRP_WX = 1 };  // named barrier
+constexpr int N_WX = 128, N_SC = 256, N_ST = 32 * ST_WARPS;
 
 // Stages: x and the scalars share a ring of NX, b and c have one of NB (they
 // are released earlier).
@@ -72,7 +73,7 @@ constexpr int SC_D = 0, SC_W = 64, SC_CUM = 160, SC_LS = 224;
 template <int DK, int DV, bool STATES>
 struct Cfg {
   static constexpr int HEADS = PT / DV;                  // heads per tile, at most
-  static constexpr int NX = STATES ? 6 : 4, NB = STATES ? 6 : 3;
+  static constexpr int NX = STATES ? 6 : 5, NB = STATES ? 6 : 3;
   static constexpr uint32_t KV = CH * DK * 2;            // b or c of a chunk
   static constexpr uint32_t X_BYTES = CH * PT * 2, K_BYTES = STATES ? KV : 2 * KV;
   static constexpr uint32_t M_BYTES = STATES ? 0 : CH * CH * 2;  // one head's scores
@@ -83,7 +84,7 @@ struct Cfg {
   static constexpr uint32_t SM_M = SM_K + NB * K_BYTES, SM_DEC = SM_M + 2 * HEADS * M_BYTES;
   static constexpr uint32_t SM_RAW = SM_DEC + NX * SC_SLOT;  // delta of four chunks to come
   static constexpr uint32_t SM_MISC = SM_RAW + 4 * HEADS * CH * 4;
-  static constexpr uint32_t BYTES = SM_MISC + 1024 + 1024;
+  static constexpr uint32_t BYTES = SM_MISC + 640 + 1024;
   // TMEM columns
   static constexpr uint32_t TM_WX = 0, TM_S = 128, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64, TM_U = TM_YM + 64,
                             TM_G = TM_U + DK, TM_END = TM_G + 64;
@@ -102,6 +103,9 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(tmap), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1) : "memory");
 }
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -132,16 +136,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// 32 columns from each of two places.
-__device__ __forceinline__ void tmem_ld_16x256b_x4x2_wait(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+// 16 columns from each of two places.
+__device__ __forceinline__ void tmem_ld_16x256b_x2x2_wait(uint32_t ta, uint32_t tb, float (&a)[8], float (&b)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(a[8]),
-        "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]), "=f"(b[0]), "=f"(b[1]),
-        "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]),
-        "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15])
+      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(b[0]),
+        "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7])
       : "r"(ta), "r"(tb)
       : "memory");
 }
@@ -330,15 +332,36 @@ struct Ctx {
   int nchunks;
 };
 
-// Tests a phase; the thread may sleep meanwhile (up to the hint, in ns).
+// Tests a phase; the thread may sleep meanwhile.  (Without a time hint: with one,
+// the wait becomes a loop of sleeps that takes issue slots from the other roles
+// and wakes late.)
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Up to 1024 tests in four instructions each.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 1024;\n"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra POLL;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -349,8 +372,7 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 __device__ __noinline__ bool wait_long(uint32_t bars, uint32_t bar, uint32_t parity) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t polls = 0; !try_wait(bar, parity); ++polls) {
-    if ((polls & 15) != 15) continue;
+  while (!poll(bar, parity)) {
     uint32_t abort;
     asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(abort) : "r"(bars + MS_ABORT) : "memory");
     if (t0 == 0) t0 = globaltimer_ns();
@@ -437,6 +459,9 @@ __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const v
   }
 #pragma unroll 1
   for (int i = 0; i < x.nchunks; ++i) {
+    if (leader && i + K::NX + 1 < x.nchunks) {  // into L2, a chunk before its load
+      for (int e = 0; e < atoms; ++e) tma_prefetch_2d(tx, col + 64 * e, tok0 + (i + K::NX + 1) * CH);
+    }
     if (i + K::NB < x.nchunks) {  // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
       if (!wait_bar(x, B_KFREE + k.st, k.ph ^ 1)) break;
       load_k();
@@ -465,7 +490,7 @@ __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const v
       }
     }
     if (i + K::NX < x.nchunks) {
-      if (!wait_bar(x, B_XFREE + s.st, s.ph ^ 1)) break;
+      if (STATES && !wait_bar(x, B_XFREE + s.st, s.ph ^ 1)) break;
       __syncwarp();
       load_x();
     }
@@ -646,10 +671,7 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
 #pragma unroll
       for (int k = 0; k < E; ++k) d[k] = softplus_f32(d[k] + bias);
     }
-    if (i >= K::NX) {  // the slot's last readers: the state, and the outputs
-      wait_bar(x, B_XFREE + s.st, s.ph ^ 1);
-      if (!STATES) wait_bar(x, B_YOUT + s.st, s.ph ^ 1);
-    }
+    if (i >= K::NX) wait_bar(x, (STATES ? B_XFREE : B_YOUT) + s.st, s.ph ^ 1);  // the slot has been read
     const int slot = s.st * (K::SC_SLOT / 4);
 #pragma unroll
     for (int k = 0; k < E; ++k)
@@ -783,22 +805,16 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
   }
 }
 
-// Eight warps turn G into M and combine the outputs, a chunk apart: the scores
-// of chunk j + 1 are made before the outputs of chunk j, whose products run
-// meanwhile.
-//   Scores: decay, step and causal mask, bf16, as the B operand of YM.  Warps q
+// G to M: decay, step and causal mask, bf16, as the B operand of YM.  Warps q
 // and q + 4 have tokens 16 q .. 16 q + 15, a head each (dv = 64) or 32 columns
 // each; what lies above the diagonal is zero.
-//   Outputs: y = e^{G_t} YI + YM + D x, over x's own tile.  Warps q and q + 4
-// have value columns 32 q .. 32 q + 31, half the tokens each.
 template <int DK, int DV>
-__device__ __forceinline__ void role_scores_out(const Ctx& x, const TcArgs& t) {
+__device__ __forceinline__ void role_scores(const Ctx& x) {
   using K = Cfg<DK, DV, false>;
-  const SsmArgs& a = t.a;
-  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, tid = threadIdx.x - 32 * W_SO, second = tid >> 7;
-  const uint32_t tl = x.tmem + ((uint32_t)(q * 32) << 16);
-  // scores: this thread's rows r0, r0 + 8 and columns cl, cl + 1 (+ 8); its row address
-  // in a 16x16 tile (four 8x8 matrices: rows 0-7, rows 8-15, then columns 8-15)
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, second = (threadIdx.x - 32 * W_SC) >> 7;
+  const uint32_t tl = x.tmem + ((uint32_t)(q * 32) << 16) + K::TM_G;
+  // this thread's rows r0, r0 + 8 and columns cl, cl + 1 (+ 8); its row address in a
+  // 16x16 tile (four 8x8 matrices: rows 0-7, rows 8-15, then columns 8-15)
   const int r0 = 16 * q + (lane >> 2), cl = 2 * (lane & 3);
   const int srow = 16 * q + ((lane >> 3) & 1) * 8 + (lane & 7), sch = (lane >> 4) & 1;
   const bool by_head = x.heads == 2;
@@ -812,102 +828,54 @@ __device__ __forceinline__ void role_scores_out(const Ctx& x, const TcArgs& t) {
     const int below = r0 + 8 * (k & 1) - (32 * (q >> 1) + 8 * (k >> 1) + cl);
     keep[k] = below > 0 ? 0xffffffffu : (below == 0 ? 0xffffu : 0u);
   }
-  // outputs
-  const int hl = DV == 64 && q >= 2 ? 1 : 0;
-  const float skip = a.D ? a.D[x.h0 + (hl < x.heads ? hl : 0)] : 0.f;
-  const float2 skip2 = make_float2(skip, skip);
-  const int row = ((lane >> 4) & 1) * 8 + (lane & 7), ch = (q & 1) * 4 + ((lane >> 3) & 1);
-  const uint32_t xl = x.sb + K::SM_X + (q >> 1) * 8192 + row * 128 + second * 4096;
-  const uint32_t sw0 = (uint32_t)(ch ^ (row & 7)) << 4, sw1 = (uint32_t)((ch + 2) ^ (row & 7)) << 4;
-  Ring<K::NX> s, so;  // stages of the scores' chunk and of the outputs'
+  Ring<K::NX> s;
 #pragma unroll 1
-  for (int i = 0; i <= x.nchunks; ++i) {
-    if (i < x.nchunks) {
-      wait_bar(x, B_G, i & 1);  // (M's buffer is free: this thread has waited for Y of chunk i - 2)
-      __syncwarp();
-      tc_fence_after();
-      const float* sc = reinterpret_cast<const float*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + sc_off;
-      const uint32_t mb = ml + (i & 1) * K::HEADS * K::M_BYTES;
-      const float2 c00 = make_float2(sc[SC_CUM + r0], sc[SC_CUM + r0]), c11 = make_float2(sc[SC_CUM + r0 + 8], sc[SC_CUM + r0 + 8]);
+  for (int i = 0; i < x.nchunks; ++i, s.next()) {
+    if (i >= 2) wait_bar(x, B_Y0 + (i & 1), ((i >> 1) - 1) & 1);  // M's buffer
+    wait_bar(x, B_G, i & 1);                        // (the scalars are there before G)
+    __syncwarp();
+    tc_fence_after();
+    const float* sc = reinterpret_cast<const float*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + sc_off;
+    const uint32_t mb = ml + (i & 1) * K::HEADS * K::M_BYTES;
+    const float2 c00 = make_float2(sc[SC_CUM + r0], sc[SC_CUM + r0]), c11 = make_float2(sc[SC_CUM + r0 + 8], sc[SC_CUM + r0 + 8]);
 #pragma unroll 1
-      for (int j = j_first; j <= q >> 1; j += j_step) {  // 32 columns at a time, so that their chains overlap
-        float g[16];
-        tmem_ld_16x256b_x4_wait(tl + K::TM_G + 32 * j, g);
+    for (int j = j_first; j <= q >> 1; j += j_step) {  // 32 columns at a time, so that their chains overlap
+      float g[16];
+      tmem_ld_16x256b_x4_wait(tl + 32 * j, g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // columns 32 j + 8 k + cl, and the next
-          const float2 ls = *reinterpret_cast<const float2*>(sc + SC_LS + 32 * j + 8 * k + cl);
-          const float2 nls = make_float2(-ls.x, -ls.y);
-          const float2 a0 = __fadd2_rn(c00, nls), a1 = __fadd2_rn(c11, nls);
-          const float2 m0 = __fmul2_rn(make_float2(g[4 * k], g[4 * k + 1]), make_float2(ex2(a0.x), ex2(a0.y)));
-          const float2 m1 = __fmul2_rn(make_float2(g[4 * k + 2], g[4 * k + 3]), make_float2(ex2(a1.x), ex2(a1.y)));
-          g[4 * k] = m0.x;
-          g[4 * k + 1] = m0.y;
-          g[4 * k + 2] = m1.x;
-          g[4 * k + 3] = m1.y;
-        }
-        uint32_t pk[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(g[2 * k], g[2 * k + 1]);
-        if (j == q >> 1) {  // cut out, not multiplied: what stands above the diagonal may be anything
-#pragma unroll
-          for (int k = 0; k < 8; ++k) pk[k] &= keep[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t t4[4] = {pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]};
-          stsm_x4(mb + (((4 * j + 2 * k + sch) ^ (srow & 7)) << 4), t4);
-        }
+      for (int k = 0; k < 4; ++k) {  // columns 32 j + 8 k + cl, and the next
+        const float2 ls = *reinterpret_cast<const float2*>(sc + SC_LS + 32 * j + 8 * k + cl);
+        const float2 nls = make_float2(-ls.x, -ls.y);
+        const float2 a0 = __fadd2_rn(c00, nls), a1 = __fadd2_rn(c11, nls);
+        const float2 m0 = __fmul2_rn(make_float2(g[4 * k], g[4 * k + 1]), make_float2(ex2(a0.x), ex2(a0.y)));
+        const float2 m1 = __fmul2_rn(make_float2(g[4 * k + 2], g[4 * k + 3]), make_float2(ex2(a1.x), ex2(a1.y)));
+        g[4 * k] = m0.x;
+        g[4 * k + 1] = m0.y;
+        g[4 * k + 2] = m1.x;
+        g[4 * k + 3] = m1.y;
       }
-      tc_fence_before();
-      fence_proxy_async_smem();
-      arrive(x, B_M0 + (i & 1));  // G may be overwritten, M is there
-      s.next();
+      uint32_t pk[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pk[k] = pack_bf16x2(g[2 * k], g[2 * k + 1]);
+      if (j == q >> 1) {  // cut out, not multiplied: what stands above the diagonal may be anything
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pk[k] &= keep[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t t4[4] = {pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]};
+        stsm_x4(mb + (((4 * j + 2 * k + sch) ^ (srow & 7)) << 4), t4);
+      }
     }
-    if (i > 0) {
-      const int o = i - 1;
-      wait_bar(x, B_Y0 + (o & 1), (o >> 1) & 1);
-      __syncwarp();
-      tc_fence_after();
-      const float* ec = reinterpret_cast<const float*>(x.sm + K::SM_DEC + so.st * K::SC_SLOT) + hl * K::SC_FLOATS + SC_CUM + cl + 32 * second;
-      const uint32_t xa = xl + so.st * K::X_BYTES;
-      float2 f[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 c = *reinterpret_cast<const float2*>(ec + 8 * k);
-        f[k] = make_float2(ex2(c.x), ex2(c.y));
-      }
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {  // 16 columns of the warp's 32
-        float yi[16], ym[16];
-        const uint32_t te = tl + K::TM_YI + 32 * second + ((uint32_t)(half * 16) << 16), xe = xa + (half ? sw1 : sw0);
-        tmem_ld_16x256b_x4x2_wait(te, te + (K::TM_YM - K::TM_YI), yi, ym);
-        if (half) {
-          tc_fence_before();
-          arrive(x, B_YFREE);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t raw[4], pk[4];
-          ldsm_x4_t(xe + k * 2048, raw);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 8 * k + 2 * j;
-            float2 y = __ffma2_rn(f[2 * k + (j >> 1)], make_float2(yi[e], yi[e + 1]), make_float2(ym[e], ym[e + 1]));
-            y = __ffma2_rn(skip2, bf16x2_f32(raw[j]), y);
-            pk[j] = pack_bf16x2(y.x, y.y);
-          }
-          stsm_x4_t(xe + k * 2048, pk);
-        }
-      }
-      fence_proxy_async_smem();
-      arrive(x, B_YOUT + so.st);
-      so.next();
-    }
+    tc_fence_before();
+    fence_proxy_async_smem();
+    arrive(x, B_M0 + (i & 1));  // G may be overwritten, M is there
   }
 }
 
-// S in registers: thread (lane p, a quarter of the key channels).  Sixteen warps,
-// so that U is free again soon: the next chunk's product waits for it.
+// S in registers: thread (lane p, a quarter of the key channels); and the
+// outputs.  Sixteen warps, so that U, YI and YM are free again soon: the next
+// chunk's products wait for them.
 template <int DK, int DV, bool STATES>
 __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
   using K = Cfg<DK, DV, STATES>;
@@ -917,7 +885,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
   const uint32_t tl = x.tmem + ((uint32_t)((w & 3) * 32) << 16);
   const int hl = DV == 64 ? p / 64 : 0;
   const bool live = hl < x.heads;
-  const int head = live ? hl : 0;
+  const int head = live ? hl : 0, hl_sc = head * K::SC_FLOATS;
   const int64_t at = ((int64_t)x.h0 + head) * DK * DV + (p & (DV - 1)) + (int64_t)n0 * DV, seq = (int64_t)a.H * DK * DV;
   float S[NC];
 #pragma unroll
@@ -951,10 +919,17 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
     }
   }
   const float* totals = reinterpret_cast<const float*>(x.sm + K::SM_MISC + MS_TOTAL) + head;
-  Ring<K::NX> s;
+  // outputs: this warp has tokens 16 part .. 16 part + 15 of value columns 32 q .. 32 q + 31
+  const int q = w & 3, part = w >> 2;
+  const float skip = !STATES && a.D ? a.D[x.h0 + head] : 0.f;
+  const float2 skip2 = make_float2(skip, skip);
+  const int row = 16 * part + ((lane >> 4) & 1) * 8 + (lane & 7), ch = (q & 1) * 4 + ((lane >> 3) & 1);
+  const uint32_t xl = x.sb + K::SM_X + (q >> 1) * 8192 + row * 128;
+  const uint32_t sw0 = (uint32_t)(ch ^ (row & 7)) << 4, sw1 = (uint32_t)((ch + 2) ^ (row & 7)) << 4;
+  Ring<K::NX> s, so;  // stages of the chunk, and of the one before it
 #pragma unroll 1
-  for (int i = 0; i < x.nchunks; ++i, s.next()) {
-    if (!STATES) {  // S before the chunk as bf16 pairs: the A operand of YI
+  for (int i = 0; STATES ? i < x.nchunks : i <= x.nchunks; ++i) {
+    if (!STATES && i < x.nchunks) {  // S before the chunk as bf16 pairs: the A operand of YI
       if (i > 0) wait_bar(x, B_SFREE, (i - 1) & 1);
       __syncwarp();
       tc_fence_after();
@@ -969,26 +944,63 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
       tc_fence_before();
       arrive(x, B_SRDY);
     }
-    wait_bar(x, B_U1, i & 1);  // (made from this chunk's scalars)
-    __syncwarp();
-    tc_fence_after();
-    const float dec = totals[s.st * 2];
-    const float2 dec2 = make_float2(dec, dec);
+    if (!STATES && i > 0) {  // y of the chunk before: e^{G_t} YI + YM + D x, over x's own tile
+      const int o = i - 1;
+      wait_bar(x, B_Y0 + (o & 1), (o >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      const float* ec = reinterpret_cast<const float*>(x.sm + K::SM_DEC + so.st * K::SC_SLOT) + hl_sc + SC_CUM + 16 * part + 2 * (lane & 3);
+      const uint32_t xa = xl + so.st * K::X_BYTES;
+      const float2 ca = *reinterpret_cast<const float2*>(ec), cb = *reinterpret_cast<const float2*>(ec + 8);
+      const float2 f[2] = {make_float2(ex2(ca.x), ex2(ca.y)), make_float2(ex2(cb.x), ex2(cb.y))};
 #pragma unroll
-    for (int k = 0; k < NC / 16; ++k) {
-      float u[16];
-      tmem_ld16(tl + K::TM_U + n0 + 16 * k, u);
+      for (int half = 0; half < 2; ++half) {  // 16 columns of the warp's 32
+        float yi[8], ym[8];
+        uint32_t raw[4], pk[4];
+        const uint32_t te = tl + K::TM_YI + 16 * part + ((uint32_t)(half * 16) << 16), xe = xa + (half ? sw1 : sw0);
+        ldsm_x4_t(xe, raw);
+        tmem_ld_16x256b_x2x2_wait(te, te + (K::TM_YM - K::TM_YI), yi, ym);
+        if (half) {
+          tc_fence_before();
+          arrive(x, B_YFREE);
+        }
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const float2 v = __ffma2_rn(make_float2(S[16 * k + j], S[16 * k + j + 1]), dec2, make_float2(u[j], u[j + 1]));
-        S[16 * k + j] = v.x;
-        S[16 * k + j + 1] = v.y;
+        for (int j = 0; j < 4; ++j) {
+          float2 y = __ffma2_rn(f[j >> 1], make_float2(yi[2 * j], yi[2 * j + 1]), make_float2(ym[2 * j], ym[2 * j + 1]));
+          y = __ffma2_rn(skip2, bf16x2_f32(raw[j]), y);
+          pk[j] = pack_bf16x2(y.x, y.y);
+        }
+        stsm_x4_t(xe, pk);
       }
+      fence_proxy_async_smem();
+      arrive(x, B_YOUT + so.st);  // (and the stage's scalars have been read)
+      so.next();
     }
-    tc_fence_before();
-    arrive(x, B_UFREE);
-    __syncwarp();
-    if (lane == 0) arrive(x, B_XFREE + s.st);
+    if (i < x.nchunks) {  // S after the chunk
+      wait_bar(x, B_U1, i & 1);  // (made from this chunk's scalars)
+      __syncwarp();
+      tc_fence_after();
+      const float dec = totals[s.st * 2];
+      const float2 dec2 = make_float2(dec, dec);
+#pragma unroll
+      for (int k = 0; k < NC / 16; ++k) {
+        float u[16];
+        tmem_ld16(tl + K::TM_U + n0 + 16 * k, u);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 v = __ffma2_rn(make_float2(S[16 * k + j], S[16 * k + j + 1]), dec2, make_float2(u[j], u[j + 1]));
+          S[16 * k + j] = v.x;
+          S[16 * k + j + 1] = v.y;
+        }
+      }
+      tc_fence_before();
+      arrive(x, B_UFREE);
+      if (STATES) {
+        __syncwarp();
+        if (lane == 0) arrive(x, B_XFREE + s.st);
+      }
+      s.next();
+    }
   }
   if (!live) return;
   float* o = nullptr;
@@ -1023,11 +1035,11 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint8_t* misc = x.sm + K::SM_MISC;
   if (tid < NUM_BARS) {
     int n = 1;
-    if (tid >= B_XFREE && tid < B_XFREE + MAXST) n = STATES ? ST_WARPS + 1 : ST_WARPS;
+    if (tid >= B_XFREE && tid < B_XFREE + MAXST) n = ST_WARPS + 1;  // (states only)
     if (!STATES && ((tid >= B_KFREE && tid < B_KFREE + MAXST) || tid == B_DRAIN)) n = 2;
-    if (tid == B_WX0 || tid == B_WX1 || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = 128;
-    if (tid == B_UFREE || tid == B_SRDY) n = 32 * ST_WARPS;
-    if (tid == B_M0 || tid == B_M1 || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = 256;
+    if (tid == B_WX0 || tid == B_WX1 || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = N_WX;
+    if (tid == B_UFREE || tid == B_SRDY || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = N_ST;
+    if (tid == B_M0 || tid == B_M1) n = N_SC;
     mbar_init(reinterpret_cast<uint64_t*>(misc) + tid, n);
     fence_mbar_init();
   }
@@ -1071,8 +1083,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
   } else if (warp >= W_ST) {
     role_state<DK, DV, STATES>(x, t);
-  } else if (warp >= W_SO) {
-    if (!STATES) role_scores_out<DK, DV>(x, t);
+  } else if (warp >= W_SC) {
+    if (!STATES) role_scores<DK, DV>(x);
   } else {
     role_wx<DK, DV, STATES>(x);
   }
