@@ -4,48 +4,54 @@
 //
 //   out_t[c] = act(bias[c] + sum_{j<K} weight[c][j] x_{t-K+1+j}[c])
 //
-// A prompt moves 2 elements per K multiply-adds, so HBM bandwidth bounds it.
-// A thread owns VEC neighbouring channels and RUN consecutive tokens: the RUN
-// loads are issued before the first product, the K - 1 inputs before the run
-// stay in registers, and a warp's accesses are 32 * VEC contiguous elements.
+// A prompt moves 2 elements per K multiply-adds, so HBM bandwidth bounds it.  A
+// thread owns VEC neighbouring channels (16 bytes) and walks RUN tokens at a
+// time: the RUN loads go out before the first product, the K - 1 inputs before
+// them stay in registers, and the weights are loaded once for all its runs.
 // Threads of a block take consecutive runs of the same channels, so that the
-// inputs before a run come from L1.
+// inputs before a thread's first run come from L1.  A run that a sequence's
+// border cuts is done token by token.
 #include "kda_layer.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int RUN = 8;    // tokens per thread
-constexpr int WARPS = 8;  // runs per block
+constexpr int RUN = 8;    // tokens per batch of loads
+constexpr int WARPS = 8;  // threads of a block in the tokens' direction
 
-template <typename T, int VEC, int K>
+// VEC channels' weights (by tap, so that neighbouring channels are neighbours)
+// and biases.
+template <int VEC, int K>
 struct Taps {
-  float w[VEC][K], b[VEC];
+  float w[K][VEC], b[VEC];
   __device__ __forceinline__ void load(const float* weight, const float* bias, int c) {
+    float f[VEC * K];
+    load_params(weight + (int64_t)c * K, f);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
+      b[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < K; ++j) w[i][j] = weight[(int64_t)(c + i) * K + j];
-      b[i] = bias ? bias[c + i] : 0.f;
+      for (int j = 0; j < K; ++j) w[j][i] = f[i * K + j];
     }
-  }
-  // rows: the K - 1 inputs before this one (oldest first), then this one
-  __device__ __forceinline__ Vec<T, VEC> apply(const Vec<T, VEC>* const (&rows)[K], int act) const {
-    float acc[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = b[i];
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      float f[VEC];
-      unpack(*rows[j], f);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[i][j], f[i], acc[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = activate(acc[i], act);
-    return pack<T, VEC>(acc);
+    if (bias) load_params(bias + c, b);
   }
 };
+
+// One output: rows[0..K-2] the inputs before, rows[K-1] the token's own.
+template <typename T, int VEC, int K, int ACT>
+__device__ __forceinline__ Vec<T, VEC> taps_apply(const Taps<VEC, K>& taps, const float (&rows)[K][VEC]) {
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = taps.b[i];
+#pragma unroll
+  for (int j = 0; j < K; ++j) vfma(acc, taps.w[j], rows[j]);
+  if constexpr (ACT == KDA_ACT_SILU) {
+    float s[VEC];
+    vsigmoid(acc, s);
+    vmul(acc, s);
+  }
+  return pack<T, VEC>(acc);
+}
 
 // Row `pos` (negative: before the sequence) of sequence n starting at token t0.
 template <typename T, int VEC, int K>
@@ -76,12 +82,12 @@ __device__ __forceinline__ void final_rows(const T* x, int64_t ldx, const T* ini
   for (int j = 0; j < K - 1; ++j) *reinterpret_cast<V*>(fin + ((int64_t)n * (K - 1) + j) * C + c) = r[j];
 }
 
-// Blocks [0, run_blocks) in y: the runs; the blocks behind them: final states.
-template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(32 * WARPS)
+// Blocks [0, run_blocks) in x: `runs` runs per thread; the blocks behind them: final states.
+template <typename T, int VEC, int K, int ACT>
+__global__ void __launch_bounds__(32 * WARPS, 2)
     conv_fwd_kernel(const T* __restrict__ x, int64_t ldx, const float* __restrict__ weight,
                     const float* __restrict__ bias, const T* init, T* __restrict__ out, T* fin, Seqs q, int C,
-                    int act, int run_blocks) {
+                    int run_blocks, int runs) {
   using V = Vec<T, VEC>;
   const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * VEC;
   if (c >= C) return;
@@ -91,109 +97,152 @@ __global__ void __launch_bounds__(32 * WARPS)
     if (n < q.N) final_rows<T, VEC, K>(x, ldx, init, fin, q, n, C, c);
     return;
   }
-  const int64_t t0 = ((int64_t)blockIdx.x * WARPS + warp) * RUN, Ttot = q.tokens();
-  if (t0 >= Ttot) return;
-  int n = q.find(t0);
-  int64_t s0 = n >= 0 ? q.begin(n) : 0, s1 = n >= 0 ? q.end(n) : q.begin(0);
-  Taps<T, VEC, K> taps;
-  if (n >= 0 && t0 + RUN <= s1) {  // the whole run lies in one sequence
-    V r[K - 1 + RUN];
-#pragma unroll
-    for (int j = 0; j < RUN; ++j) r[K - 1 + j] = *reinterpret_cast<const V*>(x + (t0 + j) * ldx + c);
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) r[j] = input_row<T, VEC, K>(x, ldx, init, s0, n, t0 - s0 - (K - 1) + j, C, c);
-    taps.load(weight, bias, c);
-#pragma unroll
-    for (int j = 0; j < RUN; ++j) {
-      const V* rows[K];
-#pragma unroll
-      for (int i = 0; i < K; ++i) rows[i] = &r[j + i];
-      *reinterpret_cast<V*>(out + (t0 + j) * C + c) = taps.apply(rows, act);
-    }
-    return;
-  }
+  const int64_t Ttot = q.tokens();
+  int64_t t = ((int64_t)blockIdx.x * WARPS + warp) * (RUN * runs);
+  if (t >= Ttot) return;
+  Taps<VEC, K> taps;
   taps.load(weight, bias, c);
+  int n = q.find(t);
+  int64_t s0 = n >= 0 ? q.begin(n) : 0, s1 = n >= 0 ? q.end(n) : q.begin(0);
+  float before[K - 1][VEC];  // the inputs before token t, where `carried`
+  bool carried = false;
 #pragma unroll 1
-  for (int64_t t = t0; t < t0 + RUN && t < Ttot; ++t) {
-    while (t >= s1 && n + 1 < q.N) {  // the next sequence that is not empty
+  for (int run = 0; run < runs && t < Ttot; ++run, t += RUN) {
+    if (n >= 0 && t >= s0 && t + RUN <= s1) {  // the whole run lies in one sequence
+      const T* xt = x + t * ldx + c;
+      V r[RUN];
+#pragma unroll
+      for (int j = 0; j < RUN; ++j) r[j] = *reinterpret_cast<const V*>(xt + j * ldx);
+      if (!carried) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) unpack(input_row<T, VEC, K>(x, ldx, init, s0, n, t - s0 - (K - 1) + j, C, c), before[j]);
+      }
+      T* ot = out + t * C + c;
+#pragma unroll
+      for (int j = 0; j < RUN; ++j) {
+        float rows[K][VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) rows[k][i] = before[k][i];
+        }
+        unpack(r[j], rows[K - 1]);
+        *reinterpret_cast<V*>(ot + (int64_t)j * C) = taps_apply<T, VEC, K, ACT>(taps, rows);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) before[k][i] = rows[k + 1][i];
+        }
+      }
+      carried = true;
+      continue;
+    }
+    carried = false;
+#pragma unroll 1
+    for (int64_t u = t; u < t + RUN && u < Ttot; ++u) {
+      while (u >= s1 && n + 1 < q.N) {  // the next sequence that is not empty
+        ++n;
+        s0 = q.begin(n);
+        s1 = q.end(n);
+      }
+      if (n < 0 || u < s0 || u >= s1) continue;  // behind the last sequence, or before the first
+      float rows[K][VEC];
+#pragma unroll
+      for (int j = 0; j < K; ++j) unpack(input_row<T, VEC, K>(x, ldx, init, s0, n, u - s0 - (K - 1) + j, C, c), rows[j]);
+      *reinterpret_cast<V*>(out + u * C + c) = taps_apply<T, VEC, K, ACT>(taps, rows);
+    }
+    while (t + RUN >= s1 && n + 1 < q.N) {  // where the next run starts
+      if (t + RUN < q.begin(n + 1)) break;
       ++n;
       s0 = q.begin(n);
       s1 = q.end(n);
     }
-    if (n < 0 || t < s0 || t >= s1) continue;  // behind the last sequence, or before the first
-    V r[K];
-    const V* rows[K];
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      r[j] = input_row<T, VEC, K>(x, ldx, init, s0, n, t - s0 - (K - 1) + j, C, c);
-      rows[j] = &r[j];
-    }
-    *reinterpret_cast<V*>(out + t * C + c) = taps.apply(rows, act);
   }
 }
 
 // One token: the K - 1 state rows and the input make the output; the state
-// moves up by one row.
-template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(128)
+// moves up by one row.  A thread takes `per` sequences with one load of its
+// weights, which are as many bytes as a sequence's rows; two are in flight.
+constexpr int STEP_THREADS = 128;
+template <typename T, int VEC, int K, int ACT>
+__global__ void __launch_bounds__(STEP_THREADS)
     conv_step_kernel(const T* __restrict__ x, int64_t ldx, const float* __restrict__ weight,
-                     const float* __restrict__ bias, T* __restrict__ state, T* __restrict__ out, int N, int C, int act) {
+                     const float* __restrict__ bias, T* __restrict__ state, T* __restrict__ out, int N, int C, int per) {
   using V = Vec<T, VEC>;
-  const int c = (blockIdx.y * 128 + threadIdx.x) * VEC;
+  const int c = (blockIdx.y * STEP_THREADS + threadIdx.x) * VEC;
   if (c >= C) return;
-  const int n = blockIdx.x;
-  V r[K];
-  T* st = state + (int64_t)n * (K - 1) * C + c;
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) r[j] = *reinterpret_cast<const V*>(st + (int64_t)j * C);
-  r[K - 1] = *reinterpret_cast<const V*>(x + n * ldx + c);
-  Taps<T, VEC, K> taps;
+  const int n0 = blockIdx.x * per, n1 = min(n0 + per, N);
+  Taps<VEC, K> taps;
   taps.load(weight, bias, c);
-  const V* rows[K];
+#pragma unroll 2
+  for (int n = n0; n < n1; ++n) {
+    V r[K];
+    T* st = state + (int64_t)n * (K - 1) * C + c;
 #pragma unroll
-  for (int j = 0; j < K; ++j) rows[j] = &r[j];
-  *reinterpret_cast<V*>(out + (int64_t)n * C + c) = taps.apply(rows, act);
+    for (int j = 0; j < K - 1; ++j) r[j] = *reinterpret_cast<const V*>(st + (int64_t)j * C);
+    r[K - 1] = *reinterpret_cast<const V*>(x + n * ldx + c);
+    float rows[K][VEC];
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) *reinterpret_cast<V*>(st + (int64_t)j * C) = r[j + 1];
+    for (int j = 0; j < K; ++j) unpack(r[j], rows[j]);
+    *reinterpret_cast<V*>(out + (int64_t)n * C + c) = taps_apply<T, VEC, K, ACT>(taps, rows);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) *reinterpret_cast<V*>(st + (int64_t)j * C) = r[j + 1];
+  }
 }
 
-template <typename T, int VEC, int K>
+constexpr int64_t BLOCKS = 148 * 8;  // blocks that keep every SM busy
+
+template <typename T, int VEC, int K, int ACT>
 cudaError_t conv_fwd(const ConvArgs& a, cudaStream_t s) {
   const Seqs q{a.cu, a.N, a.T};
   const int64_t tokens = a.cu ? a.T : (int64_t)a.N * a.T;
   const unsigned cb = (unsigned)((a.C + 32 * VEC - 1) / (32 * VEC));
-  const int runs = (int)((tokens + RUN * WARPS - 1) / (RUN * WARPS));
+  // as many runs per thread (up to 8) as leave enough blocks
+  const int64_t blocks = (tokens + RUN * WARPS - 1) / (RUN * WARPS);
+  int runs = 1;
+  while (runs < 8 && blocks * cb / (2 * runs) >= BLOCKS) runs *= 2;
+  const int run_blocks = (int)((tokens + (int64_t)RUN * WARPS * runs - 1) / ((int64_t)RUN * WARPS * runs));
   const int fins = a.fin ? (a.N + WARPS - 1) / WARPS : 0;
   const T *x = (const T*)a.x, *init = (const T*)a.init;
-  auto go = [&](int run_blocks, int fin_blocks) {
-    if (run_blocks + fin_blocks == 0) return;
-    conv_fwd_kernel<T, VEC, K><<<dim3(run_blocks + fin_blocks, cb), 32 * WARPS, 0, s>>>(
-        x, a.ldx, a.weight, a.bias, init, (T*)a.out, (T*)a.fin, q, a.C, a.act, run_blocks);
+  auto go = [&](int rb, int fb) {
+    if (rb + fb == 0) return;
+    conv_fwd_kernel<T, VEC, K, ACT><<<dim3(rb + fb, cb), 32 * WARPS, 0, s>>>(x, a.ldx, a.weight, a.bias, init, (T*)a.out,
+                                                                           (T*)a.fin, q, a.C, rb, runs);
   };
   // A state written over the initial one waits for the outputs that read it.
   if (a.fin && a.fin == a.init) {
-    go(runs, 0);
+    go(run_blocks, 0);
     go(0, fins);
   } else {
-    go(runs, fins);
+    go(run_blocks, fins);
   }
   return cudaGetLastError();
 }
 
-template <typename T, int VEC, int K>
+template <typename T, int VEC, int K, int ACT>
 cudaError_t conv_step(const ConvArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)a.N, (unsigned)((a.C + 128 * VEC - 1) / (128 * VEC)));
-  conv_step_kernel<T, VEC, K><<<grid, 128, 0, s>>>((const T*)a.x, a.ldx, a.weight, a.bias, (T*)a.fin, (T*)a.out, a.N,
-                                                   a.C, a.act);
+  const unsigned cb = (unsigned)((a.C + STEP_THREADS * VEC - 1) / (STEP_THREADS * VEC));
+  int per = 1;
+  while (per < 8 && (int64_t)a.N * cb / (2 * per) >= BLOCKS) per *= 2;
+  const dim3 grid((unsigned)((a.N + per - 1) / per), cb);
+  conv_step_kernel<T, VEC, K, ACT><<<grid, STEP_THREADS, 0, s>>>((const T*)a.x, a.ldx, a.weight, a.bias, (T*)a.fin,
+                                                                (T*)a.out, a.N, a.C, per);
   return cudaGetLastError();
+}
+
+template <bool STEP, typename T, int VEC, int K>
+cudaError_t conv_act(const ConvArgs& a, cudaStream_t s) {
+  if (a.act == KDA_ACT_SILU)
+    return STEP ? conv_step<T, VEC, K, KDA_ACT_SILU>(a, s) : conv_fwd<T, VEC, K, KDA_ACT_SILU>(a, s);
+  return STEP ? conv_step<T, VEC, K, KDA_ACT_NONE>(a, s) : conv_fwd<T, VEC, K, KDA_ACT_NONE>(a, s);
 }
 
 template <bool STEP, typename T, int VEC>
 cudaError_t conv_k(const ConvArgs& a, cudaStream_t s) {
   switch (a.K) {
-    case 2: return STEP ? conv_step<T, VEC, 2>(a, s) : conv_fwd<T, VEC, 2>(a, s);
-    case 3: return STEP ? conv_step<T, VEC, 3>(a, s) : conv_fwd<T, VEC, 3>(a, s);
-    case 4: return STEP ? conv_step<T, VEC, 4>(a, s) : conv_fwd<T, VEC, 4>(a, s);
+    case 2: return conv_act<STEP, T, VEC, 2>(a, s);
+    case 3: return conv_act<STEP, T, VEC, 3>(a, s);
+    case 4: return conv_act<STEP, T, VEC, 4>(a, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -14,25 +14,120 @@ struct alignas(N * sizeof(T)) Vec {
 
 template <typename T, int N>
 __device__ __forceinline__ void unpack(const Vec<T, N>& r, float (&f)[N]) {
+  if constexpr (sizeof(T) == 2 && N % 2 == 0) {  // a bf16 is the upper half of the fp32 with its value
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_f32(r.v[i]);
+    for (int i = 0; i < N / 2; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f32(r.v[i]);
+  }
 }
 template <typename T, int N>
 __device__ __forceinline__ Vec<T, N> pack(const float (&f)[N]) {
   Vec<T, N> r;
+  if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r);
 #pragma unroll
-  for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(f[i]);
+    for (int i = 0; i < N / 2; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(f[i]);
+  }
   return r;
 }
 
-// 1 / (1 + e^-x).  __expf overflows to inf for x < -88, where the quotient is
-// zero as it should be.
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// Elementwise arithmetic, two lanes of the fp32 pipe at a time where N is even:
+// a * b, a * s, a * b + c.
+template <int N>
+__device__ __forceinline__ void vmul(float (&a)[N], const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      a[i] = v.x; a[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] *= b[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void vscale(float (&a)[N], float s) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(s, s));
+      a[i] = v.x; a[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] *= s;
+  }
+}
+template <int N>
+__device__ __forceinline__ void vadd(float (&a)[N], const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      a[i] = v.x; a[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] += b[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void vfma(float (&c)[N], const float (&a)[N], const float (&b)[N]) {  // c += a b
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+      c[i] = v.x; c[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = fmaf(a[i], b[i], c[i]);
+  }
+}
 
-__device__ __forceinline__ float activate(float x, int act) {
-  if (act == KDA_ACT_NONE) return x;
-  const float s = sigmoid_f32(x);
-  return act == KDA_ACT_SILU ? x * s : s;
+// N neighbouring fp32 parameters; 16-byte loads where N is a multiple of 4 (their
+// offset is then one of 16 bytes, and parameters start on such a boundary).
+template <int N>
+__device__ __forceinline__ void load_params(const float* p, float (&f)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __ldg(p + i);
+  }
+}
+
+// s = sigmoid(x) = 1 / (1 + e^-x), elementwise, by the hardware's base-2
+// exponential and reciprocal (2 steps each, and |x| / 2 steps from the exponent's
+// rounding).  e^-x overflows to infinity below x = -88, where the quotient is
+// zero as it should be.
+template <int N>
+__device__ __forceinline__ void vsigmoid(const float (&x)[N], float (&s)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = x[i];
+  vscale(s, -1.4426950408889634f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(s[i]));
+  float one[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) one[i] = 1.f;
+  vadd(s, one);
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(s[i]));
 }
 
 // log(1 + e) for e in [0, 1], relative error within 4 steps: with z = e / (2 + e)

@@ -29,86 +29,148 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
   return v;
 }
 
-// TPG threads per group, NV pieces of VEC elements per thread.
-template <typename T, int VEC, int TPG, int NV>
+// v *= act(g), or v = act(v): one branch per vector.
+template <int N>
+__device__ __forceinline__ void times_act(float (&v)[N], const float (&g)[N], int act) {
+  if (act != KDA_ACT_SIGMOID) vmul(v, g);
+  if (act != KDA_ACT_NONE) {
+    float s[N];
+    vsigmoid(g, s);
+    vmul(v, s);
+  }
+}
+template <int N>
+__device__ __forceinline__ void to_act(float (&v)[N], int act) {
+  if (act == KDA_ACT_NONE) return;
+  float s[N];
+  vsigmoid(v, s);
+  if (act == KDA_ACT_SILU) {
+    vmul(v, s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = s[i];
+  }
+}
+
+// TPG threads per group, NV pieces of VEC elements per thread, U rows per team
+// (the same group of each: its parameters are loaded once, and the rows' loads
+// are in flight together).  FULL: every thread's pieces lie inside the group, and
+// every team's rows inside the tensor.
+template <typename T, int VEC, int TPG, int NV, int U, bool FULL>
 __global__ void __launch_bounds__(TPG > 256 ? TPG : 256)
     group_norm_kernel(const NormArgs a) {
   using V = Vec<T, VEC>;
   constexpr int THREADS = TPG > 256 ? TPG : 256;
   __shared__ float red[TPG > 32 ? TPG / 32 : 1];
   const int lane = threadIdx.x % TPG;
-  const int64_t units = a.rows * a.groups;
-  const int64_t u = (int64_t)blockIdx.x * (THREADS / TPG) + threadIdx.x / TPG;
-  const bool live = u < units;  // every thread stays for the team's sums
-  const int64_t row = live ? u / a.groups : 0;
-  const int g = live ? (int)(u - row * a.groups) : 0;
-  const int64_t col = (int64_t)g * a.width;
-  const T* x = (const T*)a.x + row * a.ldx + col;
-  const T* z = a.gate ? (const T*)a.gate + row * a.ldg + col : nullptr;
-
-  V xr[NV], zr[NV];
+  const int64_t team = (int64_t)blockIdx.x * (THREADS / TPG) + threadIdx.x / TPG;
+  const int64_t block = team / a.groups;  // of U rows
+  const int g = (int)(team - block * a.groups);
+  const int64_t row0 = block * U, col = (int64_t)g * a.width;
+  auto inside = [&](int u, int v) {
+    return FULL || (row0 + u < a.rows && (v * TPG + lane) * VEC < a.width);
+  };
+  V xr[U][NV], zr[U][NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = (v * TPG + lane) * VEC;
-    if (live && e < a.width) {
-      xr[v] = *reinterpret_cast<const V*>(x + e);
-      if (z) zr[v] = *reinterpret_cast<const V*>(z + e);
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = (v * TPG + lane) * VEC;
+      if (inside(u, v)) {
+        xr[u][v] = *reinterpret_cast<const V*>((const T*)a.x + (row0 + u) * a.ldx + col + e);
+        if (a.gate) zr[u][v] = *reinterpret_cast<const V*>((const T*)a.gate + (row0 + u) * a.ldg + col + e);
+      }
     }
   }
-  float f[NV][VEC];
-  float sum = 0.f;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = (v * TPG + lane) * VEC;
-    const bool in = live && e < a.width;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      f[v][i] = in ? to_f32(xr[v].v[i]) : 0.f;
-      if (in && z && a.gate_first) f[v][i] *= activate(to_f32(zr[v].v[i]), a.act);
-      sum += f[v][i];
-    }
-  }
-  const float inv = 1.f / (float)a.width;
-  const float mu = a.center ? team_sum<TPG>(sum, red) * inv : 0.f;
-  float sq = 0.f;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const bool in = live && (v * TPG + lane) * VEC < a.width;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      f[v][i] -= mu;
-      if (in) sq = fmaf(f[v][i], f[v][i], sq);
-    }
-  }
-  const float r = rsqrtf(team_sum<TPG>(sq, red) * inv + a.eps);
-  if (!live) return;
   const int64_t pcol = a.shared ? 0 : col;
-  T* out = (T*)a.out + row * ((int64_t)a.groups * a.width) + col;
+  const float inv = 1.f / (float)a.width;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = (v * TPG + lane) * VEC;
-    if (e >= a.width) continue;
-    float o[VEC];
+  for (int u = 0; u < U; ++u) {
+    // (a team's threads stay for its sums, whatever they hold)
+    float f[NV][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float n = f[v][i] * r;
-      if (a.weight) n *= a.weight[pcol + e + i];
-      if (a.bias) n += a.bias[pcol + e + i];
-      if (!z) n = activate(n, a.act);
-      else if (!a.gate_first) n *= activate(to_f32(zr[v].v[i]), a.act);
-      o[i] = n;
+    for (int v = 0; v < NV; ++v) {
+      if (inside(u, v)) {
+        unpack(xr[u][v], f[v]);
+        if (a.gate_first) {
+          float z[VEC];
+          unpack(zr[u][v], z);
+          times_act(f[v], z, a.act);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[v][i] = 0.f;
+      }
     }
-    *reinterpret_cast<V*>(out + e) = pack<T, VEC>(o);
+    if (a.center) {
+      float sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum += f[v][i];
+      const float mu = team_sum<TPG>(sum, red) * inv;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (inside(u, v)) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) f[v][i] -= mu;
+        }
+    }
+    float part[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) part[i] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) vfma(part, f[v], f[v]);
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sq += part[i];
+    const float r = rsqrtf(team_sum<TPG>(sq, red) * inv + a.eps);
+    T* out = (T*)a.out + (row0 + u) * ((int64_t)a.groups * a.width) + col;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = (v * TPG + lane) * VEC;
+      if (!inside(u, v)) continue;
+      float p[VEC];
+      vscale(f[v], r);
+      if (a.weight) {
+        load_params(a.weight + pcol + e, p);
+        vmul(f[v], p);
+      }
+      if (a.bias) {
+        load_params(a.bias + pcol + e, p);
+        vadd(f[v], p);
+      }
+      if (!a.gate) {
+        to_act(f[v], a.act);
+      } else if (!a.gate_first) {
+        unpack(zr[u][v], p);
+        times_act(f[v], p, a.act);
+      }
+      *reinterpret_cast<V*>(out + e) = pack<T, VEC>(f[v]);
+    }
   }
 }
 
+template <typename T, int VEC, int TPG, int NV, int U>
+cudaError_t go_rows(const NormArgs& a, cudaStream_t s) {
+  constexpr int THREADS = TPG > 256 ? TPG : 256, TEAMS = THREADS / TPG;
+  const int64_t teams = (a.rows + U - 1) / U * a.groups;
+  const unsigned blocks = (unsigned)((teams + TEAMS - 1) / TEAMS);
+  if (a.width == TPG * NV * VEC && a.rows % U == 0 && teams % TEAMS == 0)
+    group_norm_kernel<T, VEC, TPG, NV, U, true><<<blocks, THREADS, 0, s>>>(a);
+  else
+    group_norm_kernel<T, VEC, TPG, NV, U, false><<<blocks, THREADS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// Four rows per team where a warp or less holds a group in one piece per thread
+// and enough blocks remain, else one.
 template <typename T, int VEC, int TPG, int NV>
 cudaError_t go(const NormArgs& a, cudaStream_t s) {
-  constexpr int THREADS = TPG > 256 ? TPG : 256, TEAMS = THREADS / TPG;
-  const int64_t units = a.rows * a.groups;
-  const unsigned blocks = (unsigned)((units + TEAMS - 1) / TEAMS);
-  group_norm_kernel<T, VEC, TPG, NV><<<blocks, THREADS, 0, s>>>(a);
-  return cudaGetLastError();
+  if constexpr (TPG <= 32 && NV == 1) {
+    if (a.rows * a.groups / (256 / TPG) >= 4 * 148 * 8) return go_rows<T, VEC, TPG, NV, 4>(a, s);
+  }
+  return go_rows<T, VEC, TPG, NV, 1>(a, s);
 }
 
 // The smallest team that holds a group in few registers.

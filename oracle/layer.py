@@ -36,8 +36,8 @@ def _act(v, act):
 
 def act_error(v, act):
     """Relative error of an fp32 activation at v: the exponential is within
-    2 + 1.2 |v| steps, the quotient within 2, one product (a step is 2 U)."""
-    return 0.0 * v if act == "none" else 2 * U * (5 + 1.2 * v.abs().clamp(max=90))
+    2 + 1.2 |v| steps, the reciprocal and its argument within 3, one product (a step is 2 U)."""
+    return 0.0 * v if act == "none" else 2 * U * (6 + 1.2 * v.abs().clamp(max=90))
 
 
 def conv(x, weight, bias, init, cu, act):

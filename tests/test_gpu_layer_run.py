@@ -109,7 +109,8 @@ def test_stream_argument():
     s.wait_stream(torch.cuda.current_stream())
     out, _ = kda.kda_conv_fwd(x, p["w"], p["b"], stream=s)
     xs, b, c = out.split([H * DV, G * DK, G * DK], -1)
-    args = (xs.unflatten(-1, (H, DV)), b.unflatten(-1, (G, DK)), c.unflatten(-1, (G, DK)), delta, p["A_log"])
+    args = (xs.unflatten(-1, (H, DV)), b.unflatten(-1, (G, DK)), c.unflatten(-1, (G, DK)), delta, p["A_log"], p["D"],
+            p["dt_bias"])
     o, _ = kda.kda_ssm_fwd(*args, stream=s)
     n = kda.kda_group_norm(o, 1, stream=s)
     s.synchronize()

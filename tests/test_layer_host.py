@@ -137,15 +137,15 @@ def test_conv_binding_refusals(what, match):
 
 def test_row_strides():
     f = layer._rows
-    f32, cpu = torch.float32, torch.device("cpu")
+    f32 = torch.float32
     wide = torch.zeros(2, 3, 40)
-    assert f("x", wide[..., 8:24], (2, 3, 16), 2, f32, cpu) == 40
-    assert f("x", wide[..., 8:24].unflatten(-1, (2, 8)), (2, 3, 2, 8), 2, f32, cpu) == 40
-    assert f("x", wide, (2, 3, 40), 2, f32, cpu) == 40
-    assert f("x", wide[:1, :1], (1, 1, 40), 2, f32, cpu) == 40
-    assert f("x", wide[:, :1, :16], (2, 1, 16), 2, f32, cpu) == 120
-    assert f("x", torch.zeros(0, 3, 40), (0, 3, 40), 2, f32, cpu) == 40
-    assert f("x", torch.zeros(2, 0, 40), (2, 0, 40), 2, f32, cpu) == 40
+    assert f("x", wide[..., 8:24], (2, 3, 16), 2, f32, -1) == 40
+    assert f("x", wide[..., 8:24].unflatten(-1, (2, 8)), (2, 3, 2, 8), 2, f32, -1) == 40
+    assert f("x", wide, (2, 3, 40), 2, f32, -1) == 40
+    assert f("x", wide[:1, :1], (1, 1, 40), 2, f32, -1) == 40
+    assert f("x", wide[:, :1, :16], (2, 1, 16), 2, f32, -1) == 120
+    assert f("x", torch.zeros(0, 3, 40), (0, 3, 40), 2, f32, -1) == 40
+    assert f("x", torch.zeros(2, 0, 40), (2, 0, 40), 2, f32, -1) == 40
 
 
 # ---- the reference against other forms
