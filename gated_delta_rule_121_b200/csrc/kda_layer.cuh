@@ -219,9 +219,11 @@ struct SsmArgs {
   const int32_t* cu;
   DeviceStatus* status;
 };
-cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, bool bf16, cudaStream_t s);
+// Prompts: workspace bytes (with the status word) and launches of the two paths.
+size_t ssm_simt_workspace(int N, int64_t T, int H, int dk, int dv, bool packed);
+cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, void* workspace, bool bf16, cudaStream_t s);
 bool ssm_tc_supported(int dk, int dv, bool bf16);
-size_t ssm_tc_workspace(int N, int64_t T, int H, int G, int dk, int dv, bool packed);  // with the status word
+size_t ssm_tc_workspace(int N, int64_t T, int H, int G, int dk, int dv, bool packed);
 cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_ssm_step(const SsmArgs& a, float* state, bool bf16, cudaStream_t s);
 

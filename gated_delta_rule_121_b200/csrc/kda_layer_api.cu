@@ -77,9 +77,9 @@ kda_status_t kda_conv_step(const void* x, int64_t ldx, const float* weight, cons
 }
 
 size_t kda_ssm_fwd_workspace_size(int B, int64_t T, int H, int G, int dk, int dv, int packed, kda_dtype_t dt) {
-  if (B <= 0 || T <= 0 || H <= 0 || G <= 0 || H % G != 0 || !kda::ssm_tc_supported(dk, dv, dt == KDA_BF16))
-    return kStatusBytes;
-  return kda::ssm_tc_workspace(B, T, H, G, dk, dv, packed != 0);
+  if (B <= 0 || T <= 0 || H <= 0 || G <= 0 || H % G != 0 || !dim_ok(dk) || !dim_ok(dv)) return kStatusBytes;
+  return kda::ssm_tc_supported(dk, dv, dt == KDA_BF16) ? kda::ssm_tc_workspace(B, T, H, G, dk, dv, packed != 0)
+                                                       : kda::ssm_simt_workspace(B, T, H, dk, dv, packed != 0);
 }
 
 kda_status_t kda_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
@@ -106,8 +106,15 @@ kda_status_t kda_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb,
   if (B == 0) return KDA_OK;
   const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state,
                        B, T, H, G, dk, dv, cu_seqlens, status};
-  if (tokens > 0 && kda::ssm_tc_supported(dk, dv, dt == KDA_BF16)) return result(kda::launch_ssm_fwd_tc(a, workspace, s));
-  return result(kda::launch_ssm_fwd_simt(a, dt == KDA_BF16, s));
+  if (tokens == 0) {  // nothing to walk: the states alone
+    if (!final_state) return KDA_OK;
+    const size_t bytes = (size_t)B * H * dk * dv * sizeof(float);
+    if (!init_state) return result(cudaMemsetAsync(final_state, 0, bytes, s));
+    if (final_state == init_state) return KDA_OK;
+    return result(cudaMemcpyAsync(final_state, init_state, bytes, cudaMemcpyDeviceToDevice, s));
+  }
+  if (kda::ssm_tc_supported(dk, dv, dt == KDA_BF16)) return result(kda::launch_ssm_fwd_tc(a, workspace, s));
+  return result(kda::launch_ssm_fwd_simt(a, workspace, dt == KDA_BF16, s));
 }
 
 kda_status_t kda_ssm_step(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,

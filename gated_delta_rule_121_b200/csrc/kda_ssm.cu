@@ -5,16 +5,23 @@
 //   D_t = softplus(delta_t + dt_bias),  a_t = exp(-exp(A_log) D_t)
 //   S_t = a_t S_{t-1} + D_t b_t x_t^T,  y_t = S_t^T c_t + D x_t
 //
-// Prompt: a block owns PV value columns of one head's state and walks its
-// sequence token by token.  A thread keeps NR rows of one column in registers;
-// the RG row groups of a column are neighbouring lanes, so y is a sum over RG
-// lanes.  TB tokens at a time are staged in shared memory as fp32 while the
-// next ones are on their way to registers.  The column's chain of multiply-adds
-// bounds it (4 dk dv flops per token and head).
+// Prompt: a block owns PV value columns of one head's state and walks its piece
+// of a sequence (kda_ssm_pieces.cuh) token by token.  A thread keeps NR rows of
+// one column in registers; the RG row groups of a column are neighbouring lanes,
+// so y is a sum over RG lanes.  TB tokens at a time are staged in shared memory
+// as fp32 while the next ones are on their way to registers.
+//   Over a stage the state is kept without its decay: with G_t the sum of log
+// decays from the stage's start, S_t = e^{G_t} Z_t, Z_t = Z_{t-1} + e^{-G_t} D_t b_t
+// x_t^T, y_t = e^{G_t} Z_t^T c_t + D x_t.  That is one multiply-add per element
+// less, and one rounding of the state's decay per stage in place of one per
+// token (over thousands of slowly decaying tokens those add up to 1e-6).  Where
+// a stage decays by more than 2^-20 the plain recurrence runs instead.
+//   The column's chain of multiply-adds bounds it (4 dk dv flops per token and
+// head).
 //
 // Single token: as the KDA decode step, the state is streamed once through
 // registers; HBM bandwidth bounds it (8 dk dv bytes per head).
-#include "kda_layer.cuh"
+#include "kda_ssm_pieces.cuh"
 
 namespace kda {
 namespace {
@@ -28,37 +35,59 @@ struct ScanShape {
   static constexpr int TB = 16;                       // tokens per stage
 };
 
-template <int DK, int DV, typename IO>
+// STATES: the first pass over pieces.
+template <int DK, int DV, typename IO, bool STATES>
 __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
-    ssm_fwd_simt_kernel(const SsmArgs a) {
+    ssm_fwd_simt_kernel(const SsmArgs a, const PieceArgs pa) {
   using Sh = ScanShape<DK, DV>;
   constexpr int PV = Sh::PV, RG = Sh::RG, NR = Sh::NR, NT = Sh::NT, TB = Sh::TB;
+  static_assert(TB <= 32, "a warp scans a stage's decays");
   __shared__ float s_x[2][TB][PV];
   __shared__ alignas(16) float s_b[2][TB][DK], s_c[2][TB][DK];
-  __shared__ float s_a[2][TB], s_d[2][TB];
+  // per token: e^{G_t} and e^{-G_t} D_t where the stage decays mildly, else a_t and D_t; then e^{G} of the
+  // stage (0 where it does not)
+  __shared__ float s_e[2][TB], s_w[2][TB], s_end[2];
   const int tid = threadIdx.x, rg = tid % RG, p = tid / RG;
-  const int h = blockIdx.x % a.H, n = blockIdx.x / a.H, col0 = blockIdx.y * PV;
+  const int h = blockIdx.x % a.H, col0 = blockIdx.y * PV;
+  Piece pc;
+  if (!find_piece(pa, a.T, blockIdx.x / a.H, pc)) return;
+  if (STATES && pc.r == pc.pieces - 1) return;  // nothing follows it
   const int grp = h / (a.H / a.G);
-  const Seqs q{a.cu, a.N, a.T};
-  const int64_t t0 = q.begin(n);
-  const int64_t L = q.end(n) - t0;
+  const int64_t t0 = pc.start, L = pc.end - t0;
   const IO* x = (const IO*)a.x + (int64_t)h * DV + col0;
   const IO* b = (const IO*)a.b + (int64_t)grp * DK;
   const IO* c = (const IO*)a.c + (int64_t)grp * DK;
   IO* out = (IO*)a.out + (int64_t)h * DV + col0 + p;
-  const float rate = -expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.D ? a.D[h] : 0.f;
+  const float rate = -expf(a.A_log[h]) * 1.4426950408889634f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float skip = a.D ? a.D[h] : 0.f;
 
   // Row j of piece k of this thread: 4 (rg + RG k) + j.
+  auto row = [&](int k, int j) { return (int64_t)(4 * (rg + RG * k) + j) * DV; };
   float s[NR];
-  const int64_t sbase = ((int64_t)n * a.H + h) * DK * DV + col0 + p;
+  const int64_t at0 = (int64_t)h * DK * DV + col0 + p, seq = (int64_t)a.H * DK * DV;
+  float* slots = pa.state + at0;
+  const bool split = pc.pieces > 1;
 #pragma unroll
   for (int k = 0; k < NR / 4; ++k)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      s[4 * k + j] = a.init ? a.init[sbase + (int64_t)(4 * (rg + RG * k) + j) * DV] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      float v = 0.f;
+      if (!STATES && split) {
+        if (a.init) v = slots[pc.slot0 * seq + row(k, j)];
+        for (int r = 0; r < pc.r; ++r)
+          v = fmaf(v, exp2f(pa.decay[(int64_t)(pc.slot0 + r) * a.H + h]), slots[(pc.slot0 + r + 1) * seq + row(k, j)]);
+      } else if (a.init && (!STATES || pc.r == 0)) {
+        v = a.init[pc.n * seq + at0 + row(k, j)];
+        if (STATES) {  // kept for the second pass
+          slots[pc.slot0 * seq + row(k, j)] = v;
+          v = 0.f;
+        }
+      }
+      s[4 * k + j] = v;
+    }
 
   constexpr int XB = (TB * PV + NT - 1) / NT, KB = (TB * DK + NT - 1) / NT;
-  float rx[XB], rb[KB], rc[KB], rd = 0.f;
+  float rx[XB], rb[KB], rc[KB], rd = 0.f, total = 0.f;
   auto fetch = [&](int64_t at) {  // tokens [at, at + TB) to registers, zeros behind the end
 #pragma unroll
     for (int i = 0; i < XB; ++i) {
@@ -70,7 +99,7 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
       const int e = tid + i * NT, t = e / DK;
       const bool in = e < TB * DK && at + t < L;
       rb[i] = in ? to_f32(b[(t0 + at + t) * a.ldb + e % DK]) : 0.f;
-      rc[i] = in ? to_f32(c[(t0 + at + t) * a.ldc + e % DK]) : 0.f;
+      if (!STATES) rc[i] = in ? to_f32(c[(t0 + at + t) * a.ldc + e % DK]) : 0.f;
     }
     if (tid < TB && at + tid < L) rd = a.delta[(t0 + at + tid) * a.H + h];
   };
@@ -85,13 +114,26 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
       const int e = tid + i * NT;
       if (e < TB * DK) {
         (&s_b[buf][0][0])[e] = rb[i];
-        (&s_c[buf][0][0])[e] = rc[i];
+        if (!STATES) (&s_c[buf][0][0])[e] = rc[i];
       }
     }
-    if (tid < TB) {
-      const float d = at + tid < L ? (a.dt_bias ? softplus_f32(rd + bias) : rd) : 0.f;
-      s_d[buf][tid] = d;
-      s_a[buf][tid] = expf(rate * d);
+    if (tid < 32) {
+      const float d = tid < TB && at + tid < L ? (a.dt_bias ? softplus_f32(rd + bias) : rd) : 0.f;
+      const float g = rate * d;  // log2
+      float sum = g;
+#pragma unroll
+      for (int o = 1; o < TB; o <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (tid >= o) sum += u;
+      }
+      const float end = __shfl_sync(0xffffffffu, sum, TB - 1);
+      total += end;
+      const bool mild = end >= -20.f;
+      if (tid < TB) {
+        s_e[buf][tid] = exp2f(mild ? sum : g);
+        s_w[buf][tid] = mild ? exp2f(-sum) * d : d;
+      }
+      if (tid == 0) s_end[buf] = mild ? exp2f(end) : 0.f;
     }
   };
   if (L > 0) {
@@ -103,33 +145,56 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
     const int buf = (int)(at / TB) & 1;
     if (at + TB < L) fetch(at + TB);
     const int m = (int)(L - at < TB ? L - at : TB);
-#pragma unroll 4
-    for (int t = 0; t < m; ++t) {
-      const float xv = s_x[buf][t][p], dx = s_d[buf][t] * xv, av = s_a[buf][t];
-      float y = 0.f;
+    const float end = s_end[buf];
+    IO* o = out + (t0 + at) * ((int64_t)a.H * DV);
+    auto token = [&](int t, bool mild) {
+      const float xv = s_x[buf][t][p], dx = s_w[buf][t] * xv, ev = s_e[buf][t];
+      float y0 = 0.f, y1 = 0.f;
 #pragma unroll
       for (int k = 0; k < NR / 4; ++k) {
         const float4 bv = *reinterpret_cast<const float4*>(&s_b[buf][t][4 * (rg + RG * k)]);
-        const float4 cv = *reinterpret_cast<const float4*>(&s_c[buf][t][4 * (rg + RG * k)]);
-        const float bb[4] = {bv.x, bv.y, bv.z, bv.w}, cc[4] = {cv.x, cv.y, cv.z, cv.w};
+        const float bb[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[4 * k + j] = fmaf(av, s[4 * k + j], bb[j] * dx);
-          y = fmaf(s[4 * k + j], cc[j], y);
+        for (int j = 0; j < 4; ++j) s[4 * k + j] = mild ? fmaf(bb[j], dx, s[4 * k + j]) : fmaf(ev, s[4 * k + j], bb[j] * dx);
+        if (!STATES) {
+          const float4 cv = *reinterpret_cast<const float4*>(&s_c[buf][t][4 * (rg + RG * k)]);
+          y0 = fmaf(s[4 * k], cv.x, y0);
+          y1 = fmaf(s[4 * k + 1], cv.y, y1);
+          y0 = fmaf(s[4 * k + 2], cv.z, y0);
+          y1 = fmaf(s[4 * k + 3], cv.w, y1);
         }
       }
+      if (STATES) return;
+      float y = y0 + y1;
 #pragma unroll
-      for (int o = RG / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      if (rg == 0) out[(t0 + at + t) * ((int64_t)a.H * DV)] = from_f32<IO>(fmaf(skip, xv, y));
+      for (int q = RG / 2; q > 0; q >>= 1) y += __shfl_xor_sync(0xffffffffu, y, q);
+      if (rg == 0 && t < m) o[(int64_t)t * a.H * DV] = from_f32<IO>(fmaf(skip, xv, mild ? y * ev : y));
+    };
+    // (rows behind the end have steps of zero: they change nothing)
+    if (end != 0.f) {
+#pragma unroll 8
+      for (int t = 0; t < TB; ++t) token(t, true);
+#pragma unroll
+      for (int k = 0; k < NR; ++k) s[k] *= end;
+    } else {
+#pragma unroll 2
+      for (int t = 0; t < m; ++t) token(t, false);
     }
     if (at + TB < L) stage(buf ^ 1, at + TB);
     __syncthreads();
   }
-  if (a.fin) {
+  float* dst = nullptr;
+  if (STATES) {
+    dst = slots + (pc.slot0 + pc.r + 1) * seq;
+    if (tid == 0 && blockIdx.y == 0) pa.decay[(int64_t)(pc.slot0 + pc.r) * a.H + h] = total;
+  } else if (a.fin && pc.r == pc.pieces - 1) {
+    dst = a.fin + pc.n * seq + at0;
+  }
+  if (dst) {
 #pragma unroll
     for (int k = 0; k < NR / 4; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a.fin[sbase + (int64_t)(4 * (rg + RG * k) + j) * DV] = s[4 * k + j];
+      for (int j = 0; j < 4; ++j) dst[row(k, j)] = s[4 * k + j];
   }
 }
 
@@ -202,11 +267,22 @@ __global__ void __launch_bounds__(StepShape<DK, DV>::NT)
   }
 }
 
+PiecePlan simt_plan(int N, int64_t T, int H, int dk, int dv, bool packed) {
+  // four blocks per SM at a time; pieces of at least 128 tokens
+  return plan_pieces(N, T, H * (dv < 32 ? 1 : dv / 32), 4 * 148, 0.6, 2, H, dk, dv, packed);
+}
+
 struct Fwd {
   template <int DK, int DV, typename IO>
-  static cudaError_t go(const SsmArgs& a, float*, cudaStream_t s) {
+  static cudaError_t go(const SsmArgs& a, float* workspace, cudaStream_t s) {
     using Sh = ScanShape<DK, DV>;
-    ssm_fwd_simt_kernel<DK, DV, IO><<<dim3((unsigned)(a.N * a.H), DV / Sh::PV), Sh::NT, 0, s>>>(a);
+    const PiecePlan p = simt_plan(a.N, a.T, a.H, DK, DV, a.cu != nullptr);
+    PieceArgs pa;
+    const cudaError_t e = prepare_pieces(p, a, workspace, &pa, s);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.pieces * a.H), DV / Sh::PV);
+    if (p.split) ssm_fwd_simt_kernel<DK, DV, IO, true><<<grid, Sh::NT, 0, s>>>(a, pa);
+    ssm_fwd_simt_kernel<DK, DV, IO, false><<<grid, Sh::NT, 0, s>>>(a, pa);
     return cudaGetLastError();
   }
 };
@@ -245,8 +321,11 @@ cudaError_t by_dims(const SsmArgs& a, float* state, bool bf16, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, bool bf16, cudaStream_t s) {
-  return by_dims<Fwd>(a, nullptr, bf16, s);
+size_t ssm_simt_workspace(int N, int64_t T, int H, int dk, int dv, bool packed) {
+  return simt_plan(N, T, H, dk, dv, packed).total;
+}
+cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, void* workspace, bool bf16, cudaStream_t s) {
+  return by_dims<Fwd>(a, static_cast<float*>(workspace), bf16, s);
 }
 cudaError_t launch_ssm_step(const SsmArgs& a, float* state, bool bf16, cudaStream_t s) {
   return by_dims<Step>(a, state, bf16, s);

@@ -1,0 +1,121 @@
+// Cutting sequences into pieces (kda_ssm_pieces.cuh): the host's plan, and the
+// table of a packed batch, whose lengths are on the device.
+#include "kda_ssm_pieces.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int MAX_PIECES = 32;  // of a sequence of known length (a piece adds up the ones before it)
+
+// The pieces of a packed batch, in the sequences' order (one block; entries
+// behind the last one are marked unused).  Running sums of the pieces and of
+// the slots that sequences of several pieces take; offsets that are no
+// offsets may claim more than there is, and what lies beyond is left out.
+__global__ void __launch_bounds__(1024) ssm_piece_table_kernel(Seqs q, int64_t len, int capacity, int slots,
+                                                               PieceEntry* table) {
+  __shared__ int2 part[1024];
+  __shared__ int2 carry;
+  const int tid = threadIdx.x;
+  if (tid == 0) carry = make_int2(0, 0);
+  __syncthreads();
+  for (int n0 = 0; n0 < q.N; n0 += 1024) {
+    const int n = n0 + tid;
+    int64_t s = 0, e = 0;
+    int cnt = 0;
+    if (n < q.N) {
+      s = q.begin(n);
+      e = max(q.end(n), s);
+      cnt = (int)max((e - s + len - 1) / len, (int64_t)1);
+    }
+    const int own = cnt > 1 ? cnt : 0;
+    part[tid] = make_int2(cnt, own);
+    __syncthreads();
+    for (int o = 1; o < 1024; o <<= 1) {
+      const int2 v = tid >= o ? part[tid - o] : make_int2(0, 0);
+      __syncthreads();
+      part[tid].x += v.x;
+      part[tid].y += v.y;
+      __syncthreads();
+    }
+    const int first = carry.x + part[tid].x - cnt, slot0 = carry.y + part[tid].y - own;
+    for (int r = 0; r < cnt; ++r) {
+      const int64_t a = s + r * len;
+      if (first + r < capacity)
+        table[first + r] = {slot0 + own <= slots ? n : -1, r, cnt, slot0, (int)a, (int)min(a + len, e), {0, 0}};
+    }
+    __syncthreads();
+    if (tid == 1023) {
+      carry.x += part[1023].x;
+      carry.y += part[1023].y;
+    }
+    __syncthreads();
+  }
+  for (int i = carry.x + tid; i < capacity; i += 1024) table[i].n = -1;
+}
+
+}  // namespace
+
+PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, int least, int H, int dk, int dv,
+                      bool packed) {
+  PiecePlan p;
+  const int64_t chunks = (T + PIECE_CHUNK - 1) / PIECE_CHUNK;  // of a sequence, or of the packed total
+  if (!packed) {
+    // The number of pieces whose two passes have the fewest chunk times, in
+    // waves of blocks; 3 chunk times for a block's start, 6 for the second launch.
+    const int64_t chains = (int64_t)N * blocks;
+    auto waves = [&](int64_t n) { return (double)((n + places - 1) / places); };
+    int best = 1;
+    double cost = waves(chains) * chunks;
+    for (int r = 2; r <= MAX_PIECES && chunks / r >= least; ++r) {
+      const int64_t len = (chunks + r - 1) / r;
+      const double c = (waves(chains * r) + first * waves(chains * (r - 1))) * (len + 3) + 6;
+      if (c < cost) {
+        cost = c;
+        best = r;
+      }
+    }
+    const int64_t len = max((chunks + best - 1) / best, (int64_t)1);
+    p.per_seq = (int)max((chunks + len - 1) / len, (int64_t)1);
+    p.len = len * PIECE_CHUNK;
+    p.pieces = (int64_t)N * p.per_seq;
+    p.split = p.per_seq > 1;
+    p.slots = p.split ? p.pieces : 0;
+  } else {
+    // The lengths are on the device: pieces for twice the device's places in
+    // all, so that one long sequence does not hold the batch up.
+    int64_t len = (chunks * blocks + 2 * places - 1) / (2 * places);
+    if (len < least) len = least;
+    p.per_seq = 0;
+    p.len = len * PIECE_CHUNK;
+    p.pieces = N + T / p.len;
+    p.split = T > p.len;
+    // a sequence of L > len tokens has at most L / len + 1 < 2 L / len pieces
+    p.slots = p.split ? 2 * T / p.len : 0;
+  }
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  size_t off = 256;  // the status word
+  p.table = off;
+  if (packed) off += up((size_t)p.pieces * sizeof(PieceEntry));
+  p.decay = off;
+  off += up((size_t)p.slots * H * sizeof(float));
+  p.state = off;
+  off += (size_t)p.slots * H * dk * dv * sizeof(float);
+  p.total = off;
+  return p;
+}
+
+cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace, PieceArgs* out, cudaStream_t s) {
+  char* ws = static_cast<char*>(workspace);
+  out->len = p.len;
+  out->per_seq = p.per_seq;
+  out->table = nullptr;
+  out->decay = reinterpret_cast<float*>(ws + p.decay);
+  out->state = reinterpret_cast<float*>(ws + p.state);
+  if (!a.cu) return cudaSuccess;
+  PieceEntry* table = reinterpret_cast<PieceEntry*>(ws + p.table);
+  out->table = table;
+  ssm_piece_table_kernel<<<1, 1024, 0, s>>>(Seqs{a.cu, a.N, a.T}, p.len, (int)p.pieces, (int)p.slots, table);
+  return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -32,19 +32,16 @@
 // the skip over x's own tile; one warp each for the copies, the issue of U and
 // G, that of YI and YM, and the chunk's scalars.
 //
-// Pieces.  A sequence longer than the plan's piece length is cut into pieces
-// that run in parallel: a first pass (states only) gives each piece's own state
-// and total decay, and a block of the second pass starts from their
-// composition, S_in(r + 1) = e^{G(r)} S_in(r) + S(r).
+// Long sequences are cut into pieces that run in parallel (kda_ssm_pieces.cuh).
 #include <cuda.h>
 
-#include "kda_layer.cuh"
+#include "kda_ssm_pieces.cuh"
 #include "sm100_ptx.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int CH = 64;       // tokens per chunk
+constexpr int CH = PIECE_CHUNK;  // tokens per chunk
 constexpr int PT = 128;      // value columns per tile
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // limit of every in-kernel wait
@@ -233,91 +230,11 @@ __device__ __forceinline__ uint32_t fms_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %3;\n\tfma.rn.bf16x2 %0, %1, %2, n;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-// ------------------------------------------------------------------ pieces
-// One piece of a sequence: tokens [start, end) of sequence n, its r-th piece
-// of `pieces`.  A sequence of several pieces has `pieces` slots for states from
-// slot0 on (the initial state, then the own states of all pieces but the last)
-// and as many for decays.
-struct Piece {
-  int n, r, pieces, slot0;
-  int64_t start, end;
-};
-struct PieceEntry {  // table entry of a packed batch; n < 0: none
-  int n, r, pieces, slot0, start, end, pad[2];
-};
-
 struct TcArgs {
   SsmArgs a;
-  int hpt, tiles;        // heads per tile, tiles of 128 columns
-  int64_t piece_len;     // tokens per piece, a multiple of the chunk
-  int per_seq;           // pieces per sequence of a batch of equal lengths
-  const PieceEntry* table;
-  float* piece_state;    // [slots][H][dk][dv]
-  float* piece_decay;    // [slots][H]: log2 of a piece's total decay
+  PieceArgs p;
+  int hpt, tiles;  // heads per tile, tiles of 128 columns
 };
-
-__device__ __forceinline__ bool find_piece(const TcArgs& t, int index, Piece& p) {
-  if (t.table) {
-    const PieceEntry e = t.table[index];
-    if (e.n < 0) return false;
-    p.n = e.n; p.r = e.r; p.pieces = e.pieces; p.slot0 = e.slot0; p.start = e.start; p.end = e.end;
-    return true;
-  }
-  p.n = index / t.per_seq;
-  p.slot0 = p.n * t.per_seq;
-  p.r = index - p.n * t.per_seq;
-  p.pieces = t.per_seq;
-  const int64_t s0 = (int64_t)p.n * t.a.T;
-  p.start = s0 + p.r * t.piece_len;
-  p.end = min(p.start + t.piece_len, s0 + t.a.T);
-  return true;
-}
-
-// The pieces of a packed batch, in the sequences' order (one block; entries
-// behind the last one are marked unused).  Running sums of the pieces and of
-// the slots that sequences of several pieces take; offsets that are no
-// offsets may claim more than there is, and what lies beyond is left out.
-__global__ void __launch_bounds__(1024) ssm_piece_table_kernel(Seqs q, int64_t piece_len, int capacity, int slots,
-                                                               PieceEntry* table) {
-  __shared__ int2 part[1024];
-  __shared__ int2 carry;
-  const int tid = threadIdx.x;
-  if (tid == 0) carry = make_int2(0, 0);
-  __syncthreads();
-  for (int n0 = 0; n0 < q.N; n0 += 1024) {
-    const int n = n0 + tid;
-    int64_t s = 0, e = 0;
-    int cnt = 0;
-    if (n < q.N) {
-      s = q.begin(n);
-      e = max(q.end(n), s);
-      cnt = (int)max((e - s + piece_len - 1) / piece_len, (int64_t)1);
-    }
-    const int own = cnt > 1 ? cnt : 0;
-    part[tid] = make_int2(cnt, own);
-    __syncthreads();
-    for (int o = 1; o < 1024; o <<= 1) {
-      const int2 v = tid >= o ? part[tid - o] : make_int2(0, 0);
-      __syncthreads();
-      part[tid].x += v.x;
-      part[tid].y += v.y;
-      __syncthreads();
-    }
-    const int first = carry.x + part[tid].x - cnt, slot0 = carry.y + part[tid].y - own;
-    for (int r = 0; r < cnt; ++r) {
-      const int64_t a = s + r * piece_len;
-      if (first + r < capacity)
-        table[first + r] = {slot0 + own <= slots ? n : -1, r, cnt, slot0, (int)a, (int)min(a + piece_len, e), {0, 0}};
-    }
-    __syncthreads();
-    if (tid == 1023) {
-      carry.x += part[1023].x;
-      carry.y += part[1023].y;
-    }
-    __syncthreads();
-  }
-  for (int i = carry.x + tid; i < capacity; i += 1024) table[i].n = -1;
-}
 
 // ------------------------------------------------------------------ roles
 // Every role walks all chunks, so each block runs seven programs at once.  Their
@@ -718,7 +635,7 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
     s.next();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (STATES && l == 0 && writes) t.piece_decay[(int64_t)(x.piece.slot0 + x.piece.r) * a.H + x.h0 + h] = total;
+  if (STATES && l == 0 && writes) t.p.decay[(int64_t)(x.piece.slot0 + x.piece.r) * a.H + x.h0 + h] = total;
 }
 
 // w x as the A operand of U, in four bf16 terms.  With w = w1 + w2 + w3 (bf16
@@ -891,7 +808,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
 #pragma unroll
   for (int n = 0; n < NC; ++n) S[n] = 0.f;
   const bool split = x.piece.pieces > 1;
-  float* slots = t.piece_state + at;  // slot s of this thread's elements at slots + s * seq
+  float* slots = t.p.state + at;  // slot s of this thread's elements at slots + s * seq
   if (!STATES && live && split) {
     // the state before this piece, from the pieces before it
     const int64_t s0 = x.piece.slot0;
@@ -901,7 +818,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
     }
 #pragma unroll 1
     for (int r = 0; r < x.piece.r; ++r) {
-      const float dec = ex2(t.piece_decay[(s0 + r) * a.H + x.h0 + head]);
+      const float dec = ex2(t.p.decay[(s0 + r) * a.H + x.h0 + head]);
       const float* o = slots + (s0 + r + 1) * seq;
 #pragma unroll
       for (int n = 0; n < NC; ++n) S[n] = fmaf(S[n], dec, o[(int64_t)n * DV]);
@@ -1023,7 +940,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   extern __shared__ uint8_t smem_raw[];
   Ctx x;
   x.tile = blockIdx.x % t.tiles;
-  if (!find_piece(t, blockIdx.x / t.tiles, x.piece)) return;
+  if (!find_piece(t.p, t.a.T, blockIdx.x / t.tiles, x.piece)) return;
   if (STATES && x.piece.r == x.piece.pieces - 1) return;  // nothing follows it
   x.sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   x.sb = smem_u32(x.sm);
@@ -1128,66 +1045,12 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t width, int64_t ld, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int SMS = 148;         // of a B200
-constexpr int MIN_PIECE = 4;     // chunks in a piece, at least
-constexpr int MAX_PIECES = 32;   // of a sequence of known length (a piece adds up the ones before it)
+// Heads per tile.
+int heads_per_tile(int H, int G, int dv) { return dv == 64 && (H / G) % 2 == 0 ? 2 : 1; }
 
-struct Plan {
-  int hpt, tiles, per_seq;
-  int64_t piece_len, pieces, slots;  // pieces, slots: upper bounds for packed batches
-  bool split;
-  size_t table, decay, state, total;  // workspace offsets
-};
-
-Plan make_plan(int N, int64_t T, int H, int G, int dk, int dv, bool packed) {
-  Plan p;
-  p.hpt = dv == 64 && (H / G) % 2 == 0 ? 2 : 1;
-  p.tiles = H / p.hpt;
-  const int64_t chunks = (T + CH - 1) / CH;  // of a sequence, or of the packed total
-  const int64_t chains = (int64_t)N * p.tiles;
-  if (!packed) {
-    // Pieces in parallel against the states of all but the last of them a
-    // second time (about half the work of a chunk): the count whose two
-    // passes have the fewest chunk times, in waves of one block per SM.
-    int best = 1;
-    double cost = (double)((chains + SMS - 1) / SMS) * chunks;
-    for (int r = 2; r <= MAX_PIECES && chunks / r >= MIN_PIECE; ++r) {
-      const int64_t len = (chunks + r - 1) / r;
-      const double c = (double)((chains * r + SMS - 1) / SMS) * (len + 3) + 0.5 * ((chains * (r - 1) + SMS - 1) / SMS) * (len + 3) + 6;
-      if (c < cost) {
-        cost = c;
-        best = r;
-      }
-    }
-    const int64_t len = (chunks + best - 1) / best;
-    p.per_seq = (int)(len > 0 ? (chunks + len - 1) / len : 1);
-    if (p.per_seq < 1) p.per_seq = 1;
-    p.piece_len = (len > 0 ? len : 1) * CH;
-    p.pieces = (int64_t)N * p.per_seq;
-    p.split = p.per_seq > 1;
-    p.slots = p.split ? p.pieces : 0;
-  } else {
-    // The lengths are on the device: pieces of twice the SMs' number in all,
-    // so that one long sequence does not hold the batch up.
-    int64_t len = (chunks * p.tiles + 2 * SMS - 1) / (2 * SMS);
-    if (len < MIN_PIECE) len = MIN_PIECE;
-    p.per_seq = 0;
-    p.piece_len = len * CH;
-    p.pieces = N + T / p.piece_len;
-    p.split = T > p.piece_len;
-    // a sequence of L > len tokens has at most L / len + 1 < 2 L / len pieces
-    p.slots = p.split ? 2 * T / p.piece_len : 0;
-  }
-  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  size_t off = 256;  // the status word
-  p.table = off;
-  if (packed) off += up((size_t)p.pieces * sizeof(PieceEntry));
-  p.decay = off;
-  off += up((size_t)p.slots * H * sizeof(float));
-  p.state = off;
-  off += (size_t)p.slots * H * dk * dv * sizeof(float);
-  p.total = off;
-  return p;
+PiecePlan plan(int N, int64_t T, int H, int G, int dk, int dv, bool packed) {
+  // one block per SM; a chunk of the first pass takes about half as long as one of the second
+  return plan_pieces(N, T, H / heads_per_tile(H, G, dv), 148, 0.5, 4, H, dk, dv, packed);
 }
 
 template <int DK, int DV, bool STATES>
@@ -1197,7 +1060,7 @@ cudaError_t ready() {
 }
 
 template <int DK, int DV>
-cudaError_t launch(const TcArgs& t, const Plan& p, cudaStream_t s) {
+cudaError_t launch(const TcArgs& t, const PiecePlan& p, cudaStream_t s) {
   const SsmArgs& a = t.a;
   const int64_t rows = a.cu ? a.T : (int64_t)a.N * a.T;
   CUtensorMap tx, tb, tc, to;
@@ -1205,11 +1068,7 @@ cudaError_t launch(const TcArgs& t, const Plan& p, cudaStream_t s) {
       !make_map(&tc, a.c, (int64_t)a.G * DK, a.ldc, rows) ||
       !make_map(&to, a.out, (int64_t)a.H * DV, (int64_t)a.H * DV, rows))
     return cudaErrorInvalidValue;
-  const unsigned blocks = (unsigned)(p.pieces * p.tiles);
-  if (t.table) {
-    ssm_piece_table_kernel<<<1, 1024, 0, s>>>(Seqs{a.cu, a.N, a.T}, p.piece_len, (int)p.pieces, (int)p.slots,
-                                              const_cast<PieceEntry*>(t.table));
-  }
+  const unsigned blocks = (unsigned)(p.pieces * t.tiles);
   cudaError_t e;
   if (p.split) {
     if ((e = ready<DK, DV, true>()) != cudaSuccess) return e;
@@ -1225,21 +1084,17 @@ cudaError_t launch(const TcArgs& t, const Plan& p, cudaStream_t s) {
 bool ssm_tc_supported(int dk, int dv, bool bf16) { return bf16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
 size_t ssm_tc_workspace(int N, int64_t T, int H, int G, int dk, int dv, bool packed) {
-  return make_plan(N, T, H, G, dk, dv, packed).total;
+  return plan(N, T, H, G, dk, dv, packed).total;
 }
 
 cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s) {
-  const Plan p = make_plan(a.N, a.T, a.H, a.G, a.dk, a.dv, a.cu != nullptr);
-  char* ws = static_cast<char*>(workspace);
+  const PiecePlan p = plan(a.N, a.T, a.H, a.G, a.dk, a.dv, a.cu != nullptr);
   TcArgs t;
   t.a = a;
-  t.hpt = p.hpt;
-  t.tiles = p.tiles;
-  t.piece_len = p.piece_len;
-  t.per_seq = p.per_seq;
-  t.table = a.cu ? reinterpret_cast<const PieceEntry*>(ws + p.table) : nullptr;
-  t.piece_decay = reinterpret_cast<float*>(ws + p.decay);
-  t.piece_state = reinterpret_cast<float*>(ws + p.state);
+  t.hpt = heads_per_tile(a.H, a.G, a.dv);
+  t.tiles = a.H / t.hpt;
+  cudaError_t e = prepare_pieces(p, a, workspace, &t.p, s);
+  if (e != cudaSuccess) return e;
   if (a.dk == 128) return a.dv == 128 ? launch<128, 128>(t, p, s) : launch<128, 64>(t, p, s);
   return a.dv == 128 ? launch<64, 128>(t, p, s) : launch<64, 64>(t, p, s);
 }
