@@ -50,8 +50,7 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
   const int tid = threadIdx.x, rg = tid % RG, p = tid / RG;
   const int h = blockIdx.x % a.H, col0 = blockIdx.y * PV;
   Piece pc;
-  if (!find_piece(pa, a.T, blockIdx.x / a.H, pc)) return;
-  if (STATES && pc.r == pc.pieces - 1) return;  // nothing follows it
+  if (!find_piece<STATES>(pa, a.T, blockIdx.x / a.H, pc)) return;
   const int grp = h / (a.H / a.G);
   const int64_t t0 = pc.start, L = pc.end - t0;
   const IO* x = (const IO*)a.x + (int64_t)h * DV + col0;
@@ -66,17 +65,16 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
   float s[NR];
   const int64_t at0 = (int64_t)h * DK * DV + col0 + p, seq = (int64_t)a.H * DK * DV;
   float* slots = pa.state + at0;
-  const bool split = pc.pieces > 1;
 #pragma unroll
   for (int k = 0; k < NR / 4; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float v = 0.f;
-      if (!STATES && split) {
+      if (!STATES && pc.split) {
         if (a.init) v = slots[pc.slot0 * seq + row(k, j)];
-        for (int r = 0; r < pc.r; ++r)
+        for (int r = 0; r < pc.before; ++r)
           v = fmaf(v, exp2f(pa.decay[(int64_t)(pc.slot0 + r) * a.H + h]), slots[(pc.slot0 + r + 1) * seq + row(k, j)]);
-      } else if (a.init && (!STATES || pc.r == 0)) {
+      } else if (a.init && (!STATES || pc.first)) {
         v = a.init[pc.n * seq + at0 + row(k, j)];
         if (STATES) {  // kept for the second pass
           slots[pc.slot0 * seq + row(k, j)] = v;
@@ -185,9 +183,9 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
   }
   float* dst = nullptr;
   if (STATES) {
-    dst = slots + (pc.slot0 + pc.r + 1) * seq;
-    if (tid == 0 && blockIdx.y == 0) pa.decay[(int64_t)(pc.slot0 + pc.r) * a.H + h] = total;
-  } else if (a.fin && pc.r == pc.pieces - 1) {
+    dst = slots + (pc.slot0 + pc.before + 1) * seq;
+    if (tid == 0 && blockIdx.y == 0) pa.decay[(int64_t)(pc.slot0 + pc.before) * a.H + h] = total;
+  } else if (a.fin && pc.last) {
     dst = a.fin + pc.n * seq + at0;
   }
   if (dst) {
@@ -280,9 +278,10 @@ struct Fwd {
     PieceArgs pa;
     const cudaError_t e = prepare_pieces(p, a, workspace, &pa, s);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.pieces * a.H), DV / Sh::PV);
-    if (p.split) ssm_fwd_simt_kernel<DK, DV, IO, true><<<grid, Sh::NT, 0, s>>>(a, pa);
-    ssm_fwd_simt_kernel<DK, DV, IO, false><<<grid, Sh::NT, 0, s>>>(a, pa);
+    const unsigned slabs = DV / Sh::PV;
+    if (p.first_pass)
+      ssm_fwd_simt_kernel<DK, DV, IO, true><<<dim3((unsigned)(p.first_pass * a.H), slabs), Sh::NT, 0, s>>>(a, pa);
+    ssm_fwd_simt_kernel<DK, DV, IO, false><<<dim3((unsigned)(p.pieces * a.H), slabs), Sh::NT, 0, s>>>(a, pa);
     return cudaGetLastError();
   }
 };

@@ -5,7 +5,7 @@
 namespace kda {
 namespace {
 
-constexpr int MAX_PIECES = 32;  // of a sequence of known length (a piece adds up the ones before it)
+constexpr int MAX_PARTS = 64;  // of a sequence of known length (a piece adds up the ones before it)
 
 // The pieces of a packed batch, in the sequences' order (one block; entries
 // behind the last one are marked unused).  Running sums of the pieces and of
@@ -60,37 +60,43 @@ PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, in
   PiecePlan p;
   const int64_t chunks = (T + PIECE_CHUNK - 1) / PIECE_CHUNK;  // of a sequence, or of the packed total
   if (!packed) {
-    // The number of pieces whose two passes have the fewest chunk times, in
-    // waves of blocks; 3 chunk times for a block's start, 6 for the second launch.
+    // Pieces per sequence and parts per piece with the fewest chunk times in the
+    // two passes, in waves of blocks; 3 chunk times for a block's start and 6 for
+    // the second launch.
     const int64_t chains = (int64_t)N * blocks;
     auto waves = [&](int64_t n) { return (double)((n + places - 1) / places); };
-    int best = 1;
+    int64_t part = chunks > 0 ? chunks : 1;
+    int parts = 1;
     double cost = waves(chains) * chunks;
-    for (int r = 2; r <= MAX_PIECES && chunks / r >= least; ++r) {
-      const int64_t len = (chunks + r - 1) / r;
-      const double c = (waves(chains * r) + first * waves(chains * (r - 1))) * (len + 3) + 6;
-      if (c < cost) {
-        cost = c;
-        best = r;
+    for (int r = 2; r <= MAX_PARTS; ++r)
+      for (int q = 1; q <= 4 && r * q <= MAX_PARTS && chunks / (r * q) >= least; ++q) {
+        const int64_t len = (chunks + r * q - 1) / (r * q);
+        const double c = waves(chains * r) * (len * q + 3) + first * waves(chains * (r - 1) * q) * (len + 3) + 6;
+        if (c < cost) {
+          cost = c;
+          part = len;
+          parts = q;
+        }
       }
-    }
-    const int64_t len = max((chunks + best - 1) / best, (int64_t)1);
-    p.per_seq = (int)max((chunks + len - 1) / len, (int64_t)1);
-    p.len = len * PIECE_CHUNK;
+    p.parts = parts;
+    p.part = part * PIECE_CHUNK;
+    p.len = p.part * parts;
+    p.per_seq = (int)((chunks + part * parts - 1) / (part * parts));
+    if (p.per_seq < 1) p.per_seq = 1;
     p.pieces = (int64_t)N * p.per_seq;
-    p.split = p.per_seq > 1;
-    p.slots = p.split ? p.pieces : 0;
+    p.first_pass = (int64_t)N * (p.per_seq - 1) * parts;
+    p.slots = p.first_pass > 0 ? p.pieces * parts : 0;
   } else {
     // The lengths are on the device: pieces for twice the device's places in
     // all, so that one long sequence does not hold the batch up.
     int64_t len = (chunks * blocks + 2 * places - 1) / (2 * places);
     if (len < least) len = least;
-    p.per_seq = 0;
-    p.len = len * PIECE_CHUNK;
+    p.per_seq = p.parts = 1;
+    p.len = p.part = len * PIECE_CHUNK;
     p.pieces = N + T / p.len;
-    p.split = T > p.len;
+    p.first_pass = T > p.len ? p.pieces : 0;
     // a sequence of L > len tokens has at most L / len + 1 < 2 L / len pieces
-    p.slots = p.split ? 2 * T / p.len : 0;
+    p.slots = p.first_pass ? 2 * T / p.len : 0;
   }
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   size_t off = 256;  // the status word
@@ -107,7 +113,9 @@ PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, in
 cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace, PieceArgs* out, cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
   out->len = p.len;
+  out->part = p.part;
   out->per_seq = p.per_seq;
+  out->parts = p.parts;
   out->table = nullptr;
   out->decay = reinterpret_cast<float*>(ws + p.decay);
   out->state = reinterpret_cast<float*>(ws + p.state);

@@ -44,7 +44,6 @@ namespace {
 constexpr int CH = PIECE_CHUNK;  // tokens per chunk
 constexpr int PT = 128;      // value columns per tile
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr uint64_t WAIT_NS = 2000000000ull;  // limit of every in-kernel wait
 
 constexpr int W_WX = 0, W_SC = 4, W_ST = 12, ST_WARPS = 16, W_MOVE = W_ST + ST_WARPS, W_MMY = W_MOVE + 1, W_MMU = W_MOVE + 2, W_DEC = W_MOVE + 3,
               NWARP = W_MOVE + 4;
@@ -58,7 +57,7 @@ constexpr int MAXST = 6;
 enum Bar {
   B_XFULL = 0, B_XFREE = B_XFULL + MAXST, B_DEC = B_XFREE + MAXST, B_KFULL = B_DEC + MAXST, B_YOUT = B_KFULL + MAXST, B_XREAD = B_YOUT + MAXST,
   B_KFREE = B_XREAD + MAXST,
-  B_WX0 = B_KFREE + MAXST, B_WX1, B_U0, B_U1, B_UFREE, B_G, B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE,
+  B_WX0 = B_KFREE + MAXST, B_WX1, B_U0, B_U1, B_UFREE = B_U1 + 2, B_G = B_UFREE + 2, B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE,
   B_DRAIN, NUM_BARS
 };
 
@@ -82,9 +81,10 @@ struct Cfg {
   static constexpr uint32_t SM_RAW = SM_DEC + NX * SC_SLOT;  // delta of four chunks to come
   static constexpr uint32_t SM_MISC = SM_RAW + 4 * HEADS * CH * 4;
   static constexpr uint32_t BYTES = SM_MISC + 640 + 1024;
-  // TMEM columns
-  static constexpr uint32_t TM_WX = 0, TM_S = 128, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64, TM_U = TM_YM + 64,
-                            TM_G = TM_U + DK, TM_END = TM_G + 64;
+  // TMEM columns; the first pass has room for two U, so that one is read while the next is made
+  static constexpr int NU = STATES ? 2 : 1;
+  static constexpr uint32_t TM_WX = 0, TM_S = 128, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64,
+                            TM_U = STATES ? 128 : TM_YM + 64, TM_G = TM_U + NU * DK, TM_END = TM_G + (STATES ? 0 : 64);
   static constexpr uint32_t TM_COLS = 512;
   static_assert(NX <= MAXST && NB <= MAXST, "stages");
   static_assert(TM_END <= TM_COLS, "TMEM");
@@ -249,61 +249,43 @@ struct Ctx {
   int nchunks;
 };
 
-// Tests a phase; the thread may sleep meanwhile.  (Without a time hint: with one,
-// the wait becomes a loop of sleeps that takes issue slots from the other roles
-// and wakes late.)
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+// Bounded wait that also gives up once another role has: the first to give up
+// raises the block's flag (looked at every 256 tests), and from then on no wait of
+// the block waits long.  The roles that only compute run on over whatever is
+// there (every access stays inside its buffers) and do not look at the result;
+// the ones that start copies or products stop.  All that is waited for are the
+// block's own loads and products.  Written as one block, so that a wait that
+// finds its phase complete takes three instructions (and without a time hint:
+// with one, a wait becomes a loop of sleeps that takes issue slots from the other
+// roles and wakes late).
+constexpr uint32_t MAX_TESTS = 1u << 24;
+__device__ __forceinline__ bool wait_at(uint32_t bars, uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Up to 1024 tests in four instructions each.
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 1024;\n"
-      "POLL:\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n, f;\n\t"
+      "mov.u32 n, 0;\n"
+      "TEST:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra POLL;\n"
+      "add.u32 n, n, 1;\n\t"
+      "and.b32 f, n, 255;\n\t"
+      "setp.ne.u32 q, f, 0;\n\t"
+      "@q bra TEST;\n\t"
+      "ld.volatile.shared.u32 f, [%3];\n\t"
+      "setp.lt.u32 q, n, %4;\n\t"
+      "setp.eq.and.u32 q, f, 0, q;\n\t"
+      "@q bra TEST;\n\t"
+      "mov.u32 f, 1;\n\t"
+      "st.volatile.shared.u32 [%3], f;\n"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(bars + MS_ABORT), "n"(MAX_TESTS)
       : "memory");
   return ok != 0;
 }
-// Bounded wait that also gives up once another role has: the first to give up
-// raises the block's flag, and from then on no wait of the block waits long.
-// The roles that only compute run on over whatever is there (every access stays
-// inside its buffers); the ones that start copies or products stop.
-__device__ __noinline__ bool wait_long(uint32_t bars, uint32_t bar, uint32_t parity) {
-  uint64_t t0 = 0;
-#pragma unroll 1
-  while (!poll(bar, parity)) {
-    uint32_t abort;
-    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(abort) : "r"(bars + MS_ABORT) : "memory");
-    if (t0 == 0) t0 = globaltimer_ns();
-    if (abort != 0 || globaltimer_ns() - t0 > WAIT_NS) {
-      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(bars + MS_ABORT), "r"(1u) : "memory");
-      return false;
-    }
-  }
-  return true;
-}
 __device__ __forceinline__ bool wait_bar(const Ctx& x, int bar, uint32_t parity) {
-  const uint32_t b = x.bars + 8 * bar;
-  if (try_wait(b, parity)) return true;
-  return wait_long(x.bars, b, parity);
+  return wait_at(x.bars, x.bars + 8 * bar, parity);
 }
 __device__ __forceinline__ void arrive(const Ctx& x, int bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(x.bars + 8 * bar) : "memory");
@@ -318,9 +300,17 @@ __device__ __forceinline__ int valid_rows(const Ctx& x, int i) {
 }
 // A copy or product in flight has ended, whatever else the block gave up.
 __device__ __forceinline__ void land(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!try_wait(bar, parity) && globaltimer_ns() - t0 < WAIT_NS) {
-  }
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "TEST:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, %2;\n\t"
+      "@q bra TEST;\n"
+      "DONE:\n\t}" ::"r"(bar), "r"(parity), "n"(MAX_TESTS)
+      : "memory");
 }
 // A chunk's stage in a ring of N and the parity of its use, counted along.
 template <int N>
@@ -437,7 +427,8 @@ __device__ __forceinline__ void role_mma_u(const Ctx& x, bool leader) {
   for (int i = STATES ? 0 : -1; i < x.nchunks; ++i) {
     if (i >= 0) {
       if (STATES && !wait_bar(x, B_KFULL + kr.st, kr.ph)) return;
-      if (i > 0 && !wait_bar(x, B_UFREE, (i - 1) & 1)) return;
+      if (i >= K::NU && !wait_bar(x, B_UFREE + ((i - K::NU) & 1), ((i - K::NU) >> 1) & 1)) return;
+      const uint32_t d = x.tmem + K::TM_U + (K::NU == 2 ? (i & 1) * DK : 0);
       uint32_t bb = (b0 + (uint32_t)kr.st * (K::K_BYTES >> 4)) | (LBO << 16), ta = x.tmem + K::TM_WX;
       // by halves of the chunk, the small terms first
 #pragma unroll 1
@@ -448,10 +439,10 @@ __device__ __forceinline__ void role_mma_u(const Ctx& x, bool leader) {
           constexpr uint32_t id = idesc_bf16_f32(128, DK, 0, 1);
 #pragma unroll
           for (int term = 3; term >= 0; --term) {
-            umma_ts_lo(x.tmem + K::TM_U, ta + 16 * term, bb, id, half > 0 || term < 3);
-            umma_ts_lo(x.tmem + K::TM_U, ta + 16 * term + 8, bb + 128, id, true);
+            umma_ts_lo(d, ta + 16 * term, bb, id, half > 0 || term < 3);
+            umma_ts_lo(d, ta + 16 * term + 8, bb + 128, id, true);
           }
-          commit(x, B_U0 + half);
+          commit(x, half ? B_U1 + (i & 1) : B_U0);
         }
       }
       if (leader) {
@@ -635,7 +626,7 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
     s.next();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (STATES && l == 0 && writes) t.p.decay[(int64_t)(x.piece.slot0 + x.piece.r) * a.H + x.h0 + h] = total;
+  if (STATES && l == 0 && writes) t.p.decay[(int64_t)(x.piece.slot0 + x.piece.before) * a.H + x.h0 + h] = total;
 }
 
 // w x as the A operand of U, in four bf16 terms.  With w = w1 + w2 + w3 (bf16
@@ -688,7 +679,7 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
         w2[k] = w[32 + 4 * k];
         w3[k] = w[64 + 4 * k];
       }
-      if (i > 0) wait_bar(x, B_U0 + tb, (i - 1) & 1);
+      if (i > 0) wait_bar(x, tb ? B_U1 + ((i - 1) & 1) : B_U0, tb ? ((i - 1) >> 1) & 1 : (i - 1) & 1);
       __syncwarp();
       tc_fence_after();
 #pragma unroll 1
@@ -807,30 +798,33 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
   float S[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) S[n] = 0.f;
-  const bool split = x.piece.pieces > 1;
   float* slots = t.p.state + at;  // slot s of this thread's elements at slots + s * seq
-  if (!STATES && live && split) {
-    // the state before this piece, from the pieces before it
-    const int64_t s0 = x.piece.slot0;
-    if (a.init) {
+  const int64_t s0 = x.piece.slot0;
+  if (!STATES && live && x.piece.split) {
+    // the state before this piece, from the parts before it; a few elements and
+    // several parts at a time, so that the loads overlap
 #pragma unroll
-      for (int n = 0; n < NC; ++n) S[n] = slots[s0 * seq + (int64_t)n * DV];
-    }
-#pragma unroll 1
-    for (int r = 0; r < x.piece.r; ++r) {
-      const float dec = ex2(t.p.decay[(s0 + r) * a.H + x.h0 + head]);
-      const float* o = slots + (s0 + r + 1) * seq;
+    for (int g = 0; g < NC; g += 8) {
+      if (a.init) {
 #pragma unroll
-      for (int n = 0; n < NC; ++n) S[n] = fmaf(S[n], dec, o[(int64_t)n * DV]);
+        for (int n = 0; n < 8; ++n) S[g + n] = slots[s0 * seq + (int64_t)(g + n) * DV];
+      }
+#pragma unroll 2
+      for (int r = 0; r < x.piece.before; ++r) {
+        const float dec = ex2(t.p.decay[(s0 + r) * a.H + x.h0 + head]);
+        const float* o = slots + (s0 + r + 1) * seq + (int64_t)g * DV;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) S[g + n] = fmaf(S[g + n], dec, o[(int64_t)n * DV]);
+      }
     }
-  } else if (live && a.init && (!STATES || x.piece.r == 0)) {
+  } else if (live && a.init && (!STATES || x.piece.first)) {
     const float* o = a.init + x.piece.n * seq + at;
 #pragma unroll
     for (int n = 0; n < NC; ++n) S[n] = o[(int64_t)n * DV];
-    if (STATES) {  // kept for the second pass, whose last piece may write over the initial state
+    if (STATES) {  // kept for the second pass
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
-        slots[(int64_t)x.piece.slot0 * seq + (int64_t)n * DV] = S[n];
+        slots[s0 * seq + (int64_t)n * DV] = S[n];
         S[n] = 0.f;
       }
     }
@@ -894,7 +888,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
       so.next();
     }
     if (i < x.nchunks) {  // S after the chunk
-      wait_bar(x, B_U1, i & 1);  // (made from this chunk's scalars)
+      wait_bar(x, B_U1 + (i & 1), (i >> 1) & 1);  // (made from this chunk's scalars)
       __syncwarp();
       tc_fence_after();
       const float dec = totals[s.st * 2];
@@ -902,7 +896,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
 #pragma unroll
       for (int k = 0; k < NC / 16; ++k) {
         float u[16];
-        tmem_ld16(tl + K::TM_U + n0 + 16 * k, u);
+        tmem_ld16(tl + K::TM_U + (K::NU == 2 ? (i & 1) * DK : 0) + n0 + 16 * k, u);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float2 v = __ffma2_rn(make_float2(S[16 * k + j], S[16 * k + j + 1]), dec2, make_float2(u[j], u[j + 1]));
@@ -911,7 +905,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
         }
       }
       tc_fence_before();
-      arrive(x, B_UFREE);
+      arrive(x, B_UFREE + (i & 1));
       if (STATES) {
         __syncwarp();
         if (lane == 0) arrive(x, B_XFREE + s.st);
@@ -922,8 +916,8 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
   if (!live) return;
   float* o = nullptr;
   if (STATES)
-    o = slots + (int64_t)(x.piece.slot0 + x.piece.r + 1) * seq;
-  else if (a.fin && x.piece.r == x.piece.pieces - 1)
+    o = slots + (s0 + x.piece.before + 1) * seq;
+  else if (a.fin && x.piece.last)
     o = a.fin + x.piece.n * seq + at;
   if (o) {
 #pragma unroll
@@ -940,8 +934,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   extern __shared__ uint8_t smem_raw[];
   Ctx x;
   x.tile = blockIdx.x % t.tiles;
-  if (!find_piece(t.p, t.a.T, blockIdx.x / t.tiles, x.piece)) return;
-  if (STATES && x.piece.r == x.piece.pieces - 1) return;  // nothing follows it
+  if (!find_piece<STATES>(t.p, t.a.T, blockIdx.x / t.tiles, x.piece)) return;
   x.sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   x.sb = smem_u32(x.sm);
   x.bars = x.sb + K::SM_MISC;
@@ -955,7 +948,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid >= B_XFREE && tid < B_XFREE + MAXST) n = ST_WARPS + 1;  // (states only)
     if (!STATES && ((tid >= B_KFREE && tid < B_KFREE + MAXST) || tid == B_DRAIN)) n = 2;
     if (tid == B_WX0 || tid == B_WX1 || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = N_WX;
-    if (tid == B_UFREE || tid == B_SRDY || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = N_ST;
+    if (tid == B_UFREE || tid == B_UFREE + 1 || tid == B_SRDY || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = N_ST;
     if (tid == B_M0 || tid == B_M1) n = N_SC;
     mbar_init(reinterpret_cast<uint64_t*>(misc) + tid, n);
     fence_mbar_init();
@@ -1049,8 +1042,8 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t width, int64_t ld, int64_
 int heads_per_tile(int H, int G, int dv) { return dv == 64 && (H / G) % 2 == 0 ? 2 : 1; }
 
 PiecePlan plan(int N, int64_t T, int H, int G, int dk, int dv, bool packed) {
-  // one block per SM; a chunk of the first pass takes about half as long as one of the second
-  return plan_pieces(N, T, H / heads_per_tile(H, G, dv), 148, 0.5, 4, H, dk, dv, packed);
+  // one block per SM; a chunk of the first pass takes about 0.4 of one of the second
+  return plan_pieces(N, T, H / heads_per_tile(H, G, dv), 148, 0.4, 4, H, dk, dv, packed);
 }
 
 template <int DK, int DV, bool STATES>
@@ -1068,14 +1061,13 @@ cudaError_t launch(const TcArgs& t, const PiecePlan& p, cudaStream_t s) {
       !make_map(&tc, a.c, (int64_t)a.G * DK, a.ldc, rows) ||
       !make_map(&to, a.out, (int64_t)a.H * DV, (int64_t)a.H * DV, rows))
     return cudaErrorInvalidValue;
-  const unsigned blocks = (unsigned)(p.pieces * t.tiles);
   cudaError_t e;
-  if (p.split) {
+  if (p.first_pass) {
     if ((e = ready<DK, DV, true>()) != cudaSuccess) return e;
-    ssm_tc_kernel<DK, DV, true><<<blocks, NTHR, Cfg<DK, DV, true>::BYTES, s>>>(tx, tb, tc, to, t);
+    ssm_tc_kernel<DK, DV, true><<<(unsigned)(p.first_pass * t.tiles), NTHR, Cfg<DK, DV, true>::BYTES, s>>>(tx, tb, tc, to, t);
   }
   if ((e = ready<DK, DV, false>()) != cudaSuccess) return e;
-  ssm_tc_kernel<DK, DV, false><<<blocks, NTHR, Cfg<DK, DV, false>::BYTES, s>>>(tx, tb, tc, to, t);
+  ssm_tc_kernel<DK, DV, false><<<(unsigned)(p.pieces * t.tiles), NTHR, Cfg<DK, DV, false>::BYTES, s>>>(tx, tb, tc, to, t);
   return cudaGetLastError();
 }
 
