@@ -78,8 +78,10 @@ struct Cfg {
   // shared memory: zeros, x, zeros (the zero tiles lie below and above x: descriptor strides are positive)
   static constexpr uint32_t SM_Z0 = 0, SM_X = ZERO, SM_Z1 = SM_X + NX * X_BYTES, SM_K = SM_Z1 + ZERO;
   static constexpr uint32_t SM_M = SM_K + NB * K_BYTES, SM_DEC = SM_M + 2 * HEADS * M_BYTES;
-  static constexpr uint32_t SM_RAW = SM_DEC + NX * SC_SLOT;  // delta of four chunks to come
-  static constexpr uint32_t SM_MISC = SM_RAW + 4 * HEADS * CH * 4;
+  static constexpr uint32_t SM_RAW = SM_DEC + NX * SC_SLOT;  // delta of four chunks to come, per warp
+  static constexpr int DECS = STATES ? 2 : 1;                // warps for the scalars
+  static constexpr uint32_t RAW = 4 * HEADS * CH * 4;
+  static constexpr uint32_t SM_MISC = SM_RAW + DECS * RAW;
   static constexpr uint32_t BYTES = SM_MISC + 640 + 1024;
   // TMEM columns; the first pass has room for two U, so that one is read while the next is made
   static constexpr int NU = STATES ? 2 : 1;
@@ -90,8 +92,9 @@ struct Cfg {
   static_assert(TM_END <= TM_COLS, "TMEM");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
-// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot and head.
-constexpr uint32_t MS_TMEM = 512, MS_ABORT = 516, MS_TOTAL = 528;
+// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot and head, the log decays that
+// each of the scalars' warps has seen, by head.
+constexpr uint32_t MS_TMEM = 512, MS_ABORT = 516, MS_TOTAL = 528, MS_SUM = 576;
 static_assert(NUM_BARS * 8 <= MS_TMEM, "barrier area");
 
 // ------------------------------------------------------------------ PTX
@@ -525,9 +528,11 @@ __device__ __forceinline__ void role_mma_y(const Ctx& x, bool leader) {
 // Decays and steps of every chunk.  delta comes three chunks ahead; the steps
 // are made 32 at a time (neighbours in memory: element e of a chunk is head
 // e % heads of token e / heads); then a half-warp takes a head, a lane 4 tokens
-// (with one head in the tile the upper half-warp repeats the lower one's).
+// (with one head in the tile the upper half-warp repeats the lower one's).  In the
+// first pass two warps take every other chunk: it has little else to do, and one
+// warp's chain of dependent steps would hold it up.
 template <int DK, int DV, bool STATES>
-__device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
+__device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int which) {
   using K = Cfg<DK, DV, STATES>;
   constexpr int E = 2 * K::HEADS;  // elements per lane, at most
   const SsmArgs& a = t.a;
@@ -540,10 +545,10 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
   const int sh = x.heads - 1, per = 32 >> sh, tok = lane >> sh;  // tokens per 32 elements; this lane's first
   const float bias = soft ? a.dt_bias[x.h0 + (lane & sh)] : 0.f;
   const int64_t step = (int64_t)per * a.H;
-  const float* src = a.delta + (x.piece.start + tok) * a.H + x.h0 + (lane & sh);
-  int left = (int)(x.piece.end - x.piece.start) - tok;  // of the tokens from this lane's first one in the next fetch
+  const float* src = a.delta + (x.piece.start + which * CH + tok) * a.H + x.h0 + (lane & sh);
+  int left = (int)(x.piece.end - x.piece.start) - which * CH - tok;  // of the tokens from this lane's first one in the next fetch
   uint32_t dst = 0;
-  const uint32_t raw0 = x.sb + K::SM_RAW + lane * 4;
+  const uint32_t raw0 = x.sb + K::SM_RAW + which * K::RAW + lane * 4;
   auto fetch = [&]() {
     const float* p = src;
 #pragma unroll
@@ -556,25 +561,28 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    src += (int64_t)CH * a.H;
-    left -= CH;
+    src += (int64_t)K::DECS * CH * a.H;
+    left -= K::DECS * CH;
     dst = (dst + K::HEADS * CH * 4) & (4 * K::HEADS * CH * 4 - 1);
   };
-  const float* raw = reinterpret_cast<const float*>(x.sm + K::SM_RAW) + lane;
+  const float* raw = reinterpret_cast<const float*>(x.sm + K::SM_RAW + which * K::RAW) + lane;
   float* put_d = reinterpret_cast<float*>(x.sm + K::SM_DEC) + (lane & sh) * K::SC_FLOATS + SC_D + tok;
   float* out = reinterpret_cast<float*>(x.sm + K::SM_DEC) + h * K::SC_FLOATS + 4 * l;
   Ring<K::NX> s;
+  if (which) s.next();
+  const int mine = (x.nchunks - which + K::DECS - 1) / K::DECS;  // this warp's chunks
 #pragma unroll 1
-  for (int i = x.nchunks > 0 ? -3 : 0; i < x.nchunks; ++i) {
-    __syncwarp();  // chunk i - 1's values have been read
-    fetch();       // chunk i + 3's
-    if (i < 0) continue;
+  for (int m = mine > 0 ? -3 : 0; m < mine; ++m) {
+    __syncwarp();  // the values before have been read
+    fetch();       // three of its chunks ahead
+    if (m < 0) continue;
+    const int i = m * K::DECS + which;
     const int v = valid_rows(x, i);
     asm volatile("cp.async.wait_group 3;" ::: "memory");
     __syncwarp();
     float d[E];
 #pragma unroll
-    for (int k = 0; k < E; ++k) d[k] = raw[(i & 3) * K::HEADS * CH + 32 * k];
+    for (int k = 0; k < E; ++k) d[k] = raw[(m & 3) * K::HEADS * CH + 32 * k];
     if (soft) {  // all of a lane's elements at once: one after the other they would hold the block up
 #pragma unroll
       for (int k = 0; k < E; ++k) d[k] = softplus_f32(d[k] + bias);
@@ -624,9 +632,10 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t) {
     __syncwarp();
     if (lane == 0) arrive(x, B_DEC + s.st);
     s.next();
+    if (K::DECS == 2) s.next();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (STATES && l == 0 && writes) t.p.decay[(int64_t)(x.piece.slot0 + x.piece.before) * a.H + x.h0 + h] = total;
+  if (STATES && l == 0 && writes) reinterpret_cast<float*>(x.sm + K::SM_MISC + MS_SUM)[which * 2 + h] = total;
 }
 
 // w x as the A operand of U, in four bf16 terms.  With w = w1 + w2 + w3 (bf16
@@ -982,8 +991,10 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (warp == W_MOVE) {
       role_move<DK, DV, STATES>(x, t, &tx, &tb, &tc, &to, elect_one());
     } else if (warp == W_DEC) {
-      role_decay<DK, DV, STATES>(x, t);
-    } else if (!STATES || warp == W_MMU) {
+      role_decay<DK, DV, STATES>(x, t, 0);
+    } else if (STATES && warp == W_MMY) {
+      role_decay<DK, DV, STATES>(x, t, STATES);
+    } else {
       const bool leader = elect_one();
       if (warp == W_MMU) role_mma_u<DK, DV, STATES>(x, leader);
       else if (!STATES) role_mma_y<DK, DV>(x, leader);
@@ -1001,6 +1012,10 @@ __global__ void __launch_bounds__(NTHR, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (STATES && tid < x.heads) {
+    const float* sum = reinterpret_cast<const float*>(misc + MS_SUM) + tid;
+    t.p.decay[(int64_t)(x.piece.slot0 + x.piece.before) * t.a.H + x.h0 + tid] = sum[0] + sum[2];
+  }
   if (tid == 0 && *reinterpret_cast<volatile int*>(misc + MS_ABORT) != 0) record_error(t.a.status, KDA_ERR_TIMEOUT, 1);
   if (warp == 0) {
     tc_fence_after();
