@@ -57,7 +57,8 @@ constexpr int MAXST = 6;
 enum Bar {
   B_XFULL = 0, B_XFREE = B_XFULL + MAXST, B_DEC = B_XFREE + MAXST, B_KFULL = B_DEC + MAXST, B_YOUT = B_KFULL + MAXST, B_XREAD = B_YOUT + MAXST,
   B_KFREE = B_XREAD + MAXST,
-  B_WX0 = B_KFREE + MAXST, B_WX1, B_U0, B_U1, B_UFREE = B_U1 + 2, B_G = B_UFREE + 2, B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE,
+  B_WX = B_KFREE + MAXST, B_U = B_WX + 4, B_UFREE = B_U + 4,  // [chunk % 2][half]; [chunk % 2]
+  B_G = B_UFREE + 2, B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE,
   B_DRAIN, NUM_BARS
 };
 
@@ -83,10 +84,10 @@ struct Cfg {
   static constexpr uint32_t RAW = 4 * HEADS * CH * 4;
   static constexpr uint32_t SM_MISC = SM_RAW + DECS * RAW;
   static constexpr uint32_t BYTES = SM_MISC + 640 + 1024;
-  // TMEM columns; the first pass has room for two U, so that one is read while the next is made
+  // TMEM columns; the first pass has room for two of w x and U, so that one is read while the next is made
   static constexpr int NU = STATES ? 2 : 1;
   static constexpr uint32_t TM_WX = 0, TM_S = 128, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64,
-                            TM_U = STATES ? 128 : TM_YM + 64, TM_G = TM_U + NU * DK, TM_END = TM_G + (STATES ? 0 : 64);
+                            TM_U = STATES ? 256 : TM_YM + 64, TM_G = TM_U + NU * DK, TM_END = TM_G + (STATES ? 0 : 64);
   static constexpr uint32_t TM_COLS = 512;
   static_assert(NX <= MAXST && NB <= MAXST, "stages");
   static_assert(TM_END <= TM_COLS, "TMEM");
@@ -432,11 +433,11 @@ __device__ __forceinline__ void role_mma_u(const Ctx& x, bool leader) {
       if (STATES && !wait_bar(x, B_KFULL + kr.st, kr.ph)) return;
       if (i >= K::NU && !wait_bar(x, B_UFREE + ((i - K::NU) & 1), ((i - K::NU) >> 1) & 1)) return;
       const uint32_t d = x.tmem + K::TM_U + (K::NU == 2 ? (i & 1) * DK : 0);
-      uint32_t bb = (b0 + (uint32_t)kr.st * (K::K_BYTES >> 4)) | (LBO << 16), ta = x.tmem + K::TM_WX;
+      uint32_t bb = (b0 + (uint32_t)kr.st * (K::K_BYTES >> 4)) | (LBO << 16), ta = x.tmem + K::TM_WX + (K::NU == 2 ? (i & 1) * 128 : 0);
       // by halves of the chunk, the small terms first
 #pragma unroll 1
       for (int half = 0; half < 2; ++half, bb += 256, ta += 64) {
-        if (!wait_bar(x, B_WX0 + half, i & 1)) return;
+        if (!wait_bar(x, B_WX + 2 * (i & 1) + half, (i >> 1) & 1)) return;
         tc_fence_after();
         if (leader) {
           constexpr uint32_t id = idesc_bf16_f32(128, DK, 0, 1);
@@ -445,7 +446,7 @@ __device__ __forceinline__ void role_mma_u(const Ctx& x, bool leader) {
             umma_ts_lo(d, ta + 16 * term, bb, id, half > 0 || term < 3);
             umma_ts_lo(d, ta + 16 * term + 8, bb + 128, id, true);
           }
-          commit(x, half ? B_U1 + (i & 1) : B_U0);
+          commit(x, B_U + 2 * (i & 1) + half);
         }
       }
       if (leader) {
@@ -644,9 +645,10 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
 // x w2 leaves, is 2^-16 of the whole and is rounded to 8 bits of it.  Five packed
 // instructions per two elements; a split of the fp32 product takes twelve.
 // By halves of the chunk: a half's terms are replaced as soon as its products
-// have read them.
+// have read them.  Halves [tb0, tb1) of every chunk are this thread's: both, or in
+// the first pass, which has eight warps for it, one.
 template <int DK, int DV, bool STATES>
-__device__ __forceinline__ void role_wx(const Ctx& x) {
+__device__ __forceinline__ void role_wx(const Ctx& x, int tb0, int tb1) {
   using K = Cfg<DK, DV, STATES>;
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3, tid = threadIdx.x - 32 * W_WX;
   const uint32_t tl = x.tmem + ((uint32_t)(wq * 32) << 16) + K::TM_WX;
@@ -662,7 +664,7 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
     wait_bar(x, B_DEC + s.st, s.ph);
     wait_bar(x, B_XFULL + s.st, s.ph);
     const int v = valid_rows(x, i);
-    if (v < CH) {
+    if (!STATES && v < CH) {  // (the first pass's parts are whole chunks)
       // Rows behind the sequence's end hold other data: x and b become zero,
       // so that nothing of them (an infinity among it) reaches a product.
       wait_bar(x, B_KFULL + kr.st, kr.ph);
@@ -677,10 +679,10 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
       fence_proxy_async_smem();
       named_sync(GRP_WX, 128);
     }
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + head * K::SC_FLOATS + SC_W + (lane & 3);
-    uint32_t xa = xl + s.st * K::X_BYTES;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + head * K::SC_FLOATS + SC_W + (lane & 3) + 16 * tb0;
+    uint32_t xa = xl + s.st * K::X_BYTES + 4096 * tb0;
 #pragma unroll 1
-    for (int tb = 0; tb < 2; ++tb, w += 16, xa += 4096) {  // 32 tokens
+    for (int tb = tb0; tb < tb1; ++tb, w += 16, xa += 4096) {  // 32 tokens
       uint32_t w1[4], w2[4], w3[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -688,7 +690,7 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
         w2[k] = w[32 + 4 * k];
         w3[k] = w[64 + 4 * k];
       }
-      if (i > 0) wait_bar(x, tb ? B_U1 + ((i - 1) & 1) : B_U0, tb ? ((i - 1) >> 1) & 1 : (i - 1) & 1);
+      if (i >= K::NU) wait_bar(x, B_U + 2 * ((i - K::NU) & 1) + tb, ((i - K::NU) >> 1) & 1);
       __syncwarp();
       tc_fence_after();
 #pragma unroll 1
@@ -708,7 +710,7 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
             lo[o] = fma_bf16x2(raw[j], w3[m], fms_bf16x2(raw[j], w2[m], a2[o]));
           }
         }
-        const uint32_t ta = tl + ((uint32_t)(half * 16) << 16) + tb * 64;
+        const uint32_t ta = tl + ((uint32_t)(half * 16) << 16) + tb * 64 + (K::NU == 2 ? (i & 1) * 128 : 0);
         tmem_st_16x128b_x4(ta, a1);
         tmem_st_16x128b_x4(ta + 16, e1);
         tmem_st_16x128b_x4(ta + 32, a2);
@@ -716,7 +718,7 @@ __device__ __forceinline__ void role_wx(const Ctx& x) {
       }
       tmem_wait_st();
       tc_fence_before();
-      arrive(x, B_WX0 + tb);
+      arrive(x, B_WX + 2 * (i & 1) + tb);
       if (!STATES && tb) arrive(x, B_XREAD + s.st);  // the outputs may go over x
     }
   }
@@ -897,7 +899,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
       so.next();
     }
     if (i < x.nchunks) {  // S after the chunk
-      wait_bar(x, B_U1 + (i & 1), (i >> 1) & 1);  // (made from this chunk's scalars)
+      wait_bar(x, B_U + 2 * (i & 1) + 1, (i >> 1) & 1);  // (made from this chunk's scalars)
       __syncwarp();
       tc_fence_after();
       const float dec = totals[s.st * 2];
@@ -956,7 +958,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     int n = 1;
     if (tid >= B_XFREE && tid < B_XFREE + MAXST) n = ST_WARPS + 1;  // (states only)
     if (!STATES && ((tid >= B_KFREE && tid < B_KFREE + MAXST) || tid == B_DRAIN)) n = 2;
-    if (tid == B_WX0 || tid == B_WX1 || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = N_WX;
+    if ((tid >= B_WX && tid < B_WX + 4) || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = N_WX;
     if (tid == B_UFREE || tid == B_UFREE + 1 || tid == B_SRDY || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = N_ST;
     if (tid == B_M0 || tid == B_M1) n = N_SC;
     mbar_init(reinterpret_cast<uint64_t*>(misc) + tid, n);
@@ -1006,8 +1008,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     role_state<DK, DV, STATES>(x, t);
   } else if (warp >= W_SC) {
     if (!STATES) role_scores<DK, DV>(x);
+    else if (warp < W_SC + 4) role_wx<DK, DV, STATES>(x, 1, 2);
   } else {
-    role_wx<DK, DV, STATES>(x);
+    role_wx<DK, DV, STATES>(x, 0, STATES ? 1 : 2);
   }
   __syncwarp();
   tc_fence_before();
