@@ -60,6 +60,7 @@ kda_status_t kda_conv_fwd(const void* x, int64_t ldx, const float* weight, const
   if (st != KDA_OK) return st;
   for (const void* p : {init_state, (const void*)final_state, (const void*)cu_seqlens})
     if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+  if (out == x && tokens > 0) return KDA_ERR_INVALID_ARG;  // a token reads the ones before it
   if (B == 0) return KDA_OK;
   const kda::ConvArgs a{x, ldx, weight, bias, init_state, out, final_state, B, T, C, K, cu_seqlens, act};
   return result(kda::launch_conv_fwd(a, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));

@@ -20,8 +20,8 @@
 // Two heads share one YM accumulator: along K, head 0's x stands over a tile of
 // zeros and head 1's under one, each against its own M.
 //
-// Rounding.  x, b, c are bf16 and exact.  w x is split into three bf16 terms by
-// truncation (8 + 8 + 8 bits: exact), so that the state, which is returned and
+// Rounding.  x, b, c are bf16 and exact.  w x enters U in four bf16 terms that
+// leave out 2^-25 of it (role_wx), so that the state, which is returned and
 // carried in fp32, keeps fp32 accuracy; the state itself stays in registers and
 // takes each chunk's U by one fp32 multiply-add per element.  S and M enter the
 // output's products as bf16 (half a step each, 2^-8 relative): y is rounded to
@@ -33,6 +33,14 @@
 // G, that of YI and YM, and the chunk's scalars.
 //
 // Long sequences are cut into pieces that run in parallel (kda_ssm_pieces.cuh).
+//
+// Measured, 64K tokens, 96 heads, dk = 128, dv = 64 (48 tiles, three pieces): 0.88
+// ms, of which 0.22 the first pass (0.95 us a chunk) and 0.66 the second (1.95 us
+// a chunk).  The second pass is bound by the instructions around its products:
+// issue slots 64 % busy, the shared-memory pipe ~80 % (the roles' accesses and the
+// operands'), the tensor pipe 54 %, DRAM 31 %.  A state of 64 columns per thread
+// in eight warps (fewer instructions in all) does not fit the registers that
+// remain.
 #include <cuda.h>
 
 #include "kda_ssm_pieces.cuh"
@@ -42,24 +50,44 @@ namespace kda {
 namespace {
 
 constexpr int CH = PIECE_CHUNK;  // tokens per chunk
-constexpr int PT = 128;      // value columns per tile
+constexpr int PT = 128;          // value columns per tile
 constexpr float LOG2E = 1.4426950408889634f;
 
-constexpr int W_WX = 0, W_SC = 4, W_ST = 12, ST_WARPS = 16, W_MOVE = W_ST + ST_WARPS, W_MMY = W_MOVE + 1, W_MMU = W_MOVE + 2, W_DEC = W_MOVE + 3,
-              NWARP = W_MOVE + 4;
+// First warps of the roles.
+constexpr int W_WX = 0, W_SC = 4, W_ST = 12, ST_WARPS = 16, W_MOVE = W_ST + ST_WARPS, W_MMY = W_MOVE + 1,
+              W_MMU = W_MOVE + 2, W_DEC = W_MOVE + 3, NWARP = W_MOVE + 4;
 constexpr int NTHR = 32 * NWARP;
-enum { GRP_WX = 1 };  // named barrier
-constexpr int N_WX = 128, N_SC = 256, N_ST = 32 * ST_WARPS;
+constexpr int N_WX = 128, N_SC = 256, N_ST = 32 * ST_WARPS;  // threads
+constexpr int GRP_WX = 1;                                    // named barrier of wx
 
-// Stages: x and the scalars share a ring of NX, b and c have one of NB (they
-// are released earlier).
+// Hand-offs.  Per stage: XFULL x has landed, XFREE (first pass) it has been used,
+// DEC the scalars are there, KFULL / KFREE the same of b and c, XREAD wx has read
+// x, YOUT y stands in x's place.  Per chunk: WX half of w x is there, U it has been
+// used (and with the second half U is there), UFREE U has been read, G scores' Gram
+// is there, M scores are there (and G has been read), SRDY / SFREE S as bf16 is
+// there / has been used, Y both parts of y are there, YFREE they have been read.
+// A barrier whose waiter can fall a phase behind is doubled by the chunk's parity.
+// x and the scalars share a ring of NX stages, b and c have one of NB.
 constexpr int MAXST = 6;
 enum Bar {
-  B_XFULL = 0, B_XFREE = B_XFULL + MAXST, B_DEC = B_XFREE + MAXST, B_KFULL = B_DEC + MAXST, B_YOUT = B_KFULL + MAXST, B_XREAD = B_YOUT + MAXST,
-  B_KFREE = B_XREAD + MAXST,
-  B_WX = B_KFREE + MAXST, B_U = B_WX + 4, B_UFREE = B_U + 4,  // [chunk % 2][half]; [chunk % 2]
-  B_G = B_UFREE + 2, B_SRDY, B_SFREE, B_M0, B_M1, B_Y0, B_Y1, B_YFREE,
-  B_DRAIN, NUM_BARS
+  B_XFULL = 0,
+  B_XFREE = B_XFULL + MAXST,
+  B_DEC = B_XFREE + MAXST,
+  B_KFULL = B_DEC + MAXST,
+  B_KFREE = B_KFULL + MAXST,
+  B_XREAD = B_KFREE + MAXST,
+  B_YOUT = B_XREAD + MAXST,
+  B_WX = B_YOUT + MAXST,  // [chunk % 2][half]
+  B_U = B_WX + 4,         // [chunk % 2][half]
+  B_UFREE = B_U + 4,      // [chunk % 2]
+  B_M = B_UFREE + 2,      // [chunk % 2]
+  B_Y = B_M + 2,          // [chunk % 2]
+  B_G = B_Y + 2,
+  B_SRDY,
+  B_SFREE,
+  B_YFREE,
+  B_DRAIN,
+  NUM_BARS
 };
 
 // Scalars of a chunk, per head, at these 32-bit words: the steps D_s; the
@@ -93,8 +121,8 @@ struct Cfg {
   static_assert(TM_END <= TM_COLS, "TMEM");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
-// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot and head, the log decays that
-// each of the scalars' warps has seen, by head.
+// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot
+// and head, the log decays that each of the scalars' warps has seen, by head.
 constexpr uint32_t MS_TMEM = 512, MS_ABORT = 516, MS_TOTAL = 528, MS_SUM = 576;
 static_assert(NUM_BARS * 8 <= MS_TMEM, "barrier area");
 
@@ -234,6 +262,7 @@ __device__ __forceinline__ uint32_t fms_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %3;\n\tfma.rn.bf16x2 %0, %1, %2, n;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+
 struct TcArgs {
   SsmArgs a;
   PieceArgs p;
@@ -244,7 +273,7 @@ struct TcArgs {
 // Every role walks all chunks, so each block runs seven programs at once.  Their
 // loops are kept rolled and short: the instruction caches hold all of them only
 // then (with the roles unrolled, warps waited for instructions most of the
-// time, 3.6 us a chunk).
+// time, 3.6 us a chunk).  For the same reason the waits are short and inline.
 struct Ctx {
   uint8_t* sm;
   uint32_t sb, tmem, bars;   // shared-window addresses of sm and of the barriers; TMEM base
@@ -262,7 +291,7 @@ struct Ctx {
 // finds its phase complete takes three instructions (and without a time hint:
 // with one, a wait becomes a loop of sleeps that takes issue slots from the other
 // roles and wakes late).
-constexpr uint32_t MAX_TESTS = 1u << 24;
+constexpr uint32_t MAX_TESTS = 1u << 23;  // some tenths of a second: a test takes about 50 ns
 __device__ __forceinline__ bool wait_at(uint32_t bars, uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -459,7 +488,7 @@ __device__ __forceinline__ void role_mma_u(const Ctx& x, bool leader) {
     if (!STATES && i + 1 < x.nchunks) {
       // the scalars as well, so that the scores' role has one wait for all
       if (!wait_bar(x, B_KFULL + kn.st, kn.ph) || !wait_bar(x, B_DEC + sn.st, sn.ph)) return;
-      if (i >= 0 && !wait_bar(x, B_M0 + (i & 1), (i >> 1) & 1)) return;
+      if (i >= 0 && !wait_bar(x, B_M + (i & 1), (i >> 1) & 1)) return;
       tc_fence_after();
       if (leader) {
         constexpr uint32_t id = idesc_bf16_f32(64, 64, 0, 0);
@@ -503,7 +532,7 @@ __device__ __forceinline__ void role_mma_y(const Ctx& x, bool leader) {
       commit(x, B_KFREE + kr.st);
     }
     // (and x read by wx, since y goes over it once Y is there)
-    if (!wait_bar(x, B_M0 + (i & 1), (i >> 1) & 1) || !wait_bar(x, B_XREAD + s.st, s.ph)) return;
+    if (!wait_bar(x, B_M + (i & 1), (i >> 1) & 1) || !wait_bar(x, B_XREAD + s.st, s.ph)) return;
     tc_fence_after();
     if (leader) {
       constexpr uint32_t id = idesc_bf16_f32(128, 64, 1, 0);
@@ -521,7 +550,7 @@ __device__ __forceinline__ void role_mma_y(const Ctx& x, bool leader) {
           umma_ss_lo(tm + K::TM_YM, z0 | ((xk - z0) << 16), m + (K::M_BYTES >> 4) + k * 2, id, 1);
         }
       }
-      commit(x, B_Y0 + (i & 1));
+      commit(x, B_Y + (i & 1));
     }
   }
 }
@@ -750,7 +779,7 @@ __device__ __forceinline__ void role_scores(const Ctx& x) {
   Ring<K::NX> s;
 #pragma unroll 1
   for (int i = 0; i < x.nchunks; ++i, s.next()) {
-    if (i >= 2) wait_bar(x, B_Y0 + (i & 1), ((i >> 1) - 1) & 1);  // M's buffer
+    if (i >= 2) wait_bar(x, B_Y + (i & 1), ((i >> 1) - 1) & 1);  // M's buffer
     wait_bar(x, B_G, i & 1);                        // (the scalars are there before G)
     __syncwarp();
     tc_fence_after();
@@ -788,7 +817,7 @@ __device__ __forceinline__ void role_scores(const Ctx& x) {
     }
     tc_fence_before();
     fence_proxy_async_smem();
-    arrive(x, B_M0 + (i & 1));  // G may be overwritten, M is there
+    arrive(x, B_M + (i & 1));  // G may be overwritten, M is there
   }
 }
 
@@ -868,7 +897,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
     }
     if (!STATES && i > 0) {  // y of the chunk before: e^{G_t} YI + YM + D x, over x's own tile
       const int o = i - 1;
-      wait_bar(x, B_Y0 + (o & 1), (o >> 1) & 1);
+      wait_bar(x, B_Y + (o & 1), (o >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       const float* ec = reinterpret_cast<const float*>(x.sm + K::SM_DEC + so.st * K::SC_SLOT) + hl_sc + SC_CUM + 16 * part + 2 * (lane & 3);
@@ -959,8 +988,10 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid >= B_XFREE && tid < B_XFREE + MAXST) n = ST_WARPS + 1;  // (states only)
     if (!STATES && ((tid >= B_KFREE && tid < B_KFREE + MAXST) || tid == B_DRAIN)) n = 2;
     if ((tid >= B_WX && tid < B_WX + 4) || (tid >= B_XREAD && tid < B_XREAD + MAXST)) n = N_WX;
-    if (tid == B_UFREE || tid == B_UFREE + 1 || tid == B_SRDY || tid == B_YFREE || (tid >= B_YOUT && tid < B_YOUT + MAXST)) n = N_ST;
-    if (tid == B_M0 || tid == B_M1) n = N_SC;
+    if (tid == B_UFREE || tid == B_UFREE + 1 || tid == B_SRDY || tid == B_YFREE ||
+        (tid >= B_YOUT && tid < B_YOUT + MAXST))
+      n = N_ST;
+    if (tid == B_M || tid == B_M + 1) n = N_SC;
     mbar_init(reinterpret_cast<uint64_t*>(misc) + tid, n);
     fence_mbar_init();
   }

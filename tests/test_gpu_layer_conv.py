@@ -98,8 +98,19 @@ def test_large_values_and_no_tokens():
     assert kda.kda_conv_step(x[0, :0], randn(g, 24, 4), None, x.new_zeros(0, 3, 24)).shape == (0, 24)
 
 
+def test_offsets_beyond_32_bits():
+    """Rows of a tensor of more than 2^31 elements: the bits of the dense rows' result."""
+    wide = torch.empty(1, 70000, 32768, dtype=BF16, device="cuda")
+    g = gen(9)
+    for C in (64, 63):
+        x, w = randn(g, 1, 70000, C, dtype=BF16), randn(g, C, 4)
+        wide[..., -C:] = x
+        for a, b in zip(kda.kda_conv_fwd(wide[..., -C:], w), kda.kda_conv_fwd(x, w)):
+            assert torch.equal(a, b)
+
+
 def test_long_rows():
-    """Many runs per sequence, a 64-bit row offset's worth of tokens is left to the arithmetic."""
+    """Many runs per sequence."""
     g = gen(6)
     x = randn(g, 1, 3001, 520, dtype=BF16)
     check(x, randn(g, 520, 4), randn(g, 520), None, offsets([1000, 3, 1998]), "silu")

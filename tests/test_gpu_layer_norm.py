@@ -86,3 +86,12 @@ def test_rows_of_zeros_constants_and_large_values():
 
 def test_no_rows():
     assert kda.kda_group_norm(torch.empty(0, 3, 64, device="cuda", dtype=BF16), 2).shape == (0, 3, 64)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of a tensor of more than 2^31 elements: the bits of the dense rows' result."""
+    wide = torch.empty(70000, 32768, dtype=BF16, device="cuda")
+    x = randn(gen(15), 70000, 64, dtype=BF16)
+    wide[:, -64:] = x
+    assert torch.equal(kda.kda_group_norm(wide[:, -64:], 4), kda.kda_group_norm(x, 4))
+    assert torch.equal(kda.kda_group_norm(x, 4, None, None, wide[:, -64:]), kda.kda_group_norm(x, 4, None, None, x))

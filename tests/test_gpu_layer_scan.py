@@ -200,3 +200,44 @@ def test_no_tokens():
     out, fin = run(none, init, None)
     assert out.shape == (2, 0, 2, 64) and torch.equal(fin, init)
     assert not bool(run(none, None, None)[1].any())
+
+
+@pytest.mark.parametrize("dtype,H,G,dk,dv", [(BF16, 2, 1, 128, 64), (BF16, 3, 3, 64, 64), (BF16, 1, 1, 128, 128),
+                                             (F32, 2, 2, 32, 16)])
+@pytest.mark.parametrize("lengths", [None, [1, 1700, 0, 64, 900]])
+def test_long_sequences_in_place(dtype, H, G, dk, dv, lengths):
+    """Split sequences whose final states go over their initial ones: the bits of
+    the call that keeps them apart."""
+    T = 2665 if lengths else 1500
+    d, g = scan_inputs(71, (1 if lengths else 2, T), H, G, dk, dv, dtype, rate=0.02)
+    cu = offsets(lengths) if lengths else None
+    init = randn(g, len(lengths) if lengths else 2, H, dk, dv)
+    out, fin = run(d, init, cu)
+    state = init.clone()
+    out2, _ = run(d, state, cu, final_state=state)
+    assert torch.equal(out, out2) and torch.equal(fin, state)
+    assert not torch.equal(fin, init)
+
+
+@pytest.mark.parametrize("T", [255, 256, 257, 511, 512, 513, 1025])
+@pytest.mark.parametrize("dtype,dv", [(BF16, 64), (F32, 16)])
+def test_lengths_around_the_pieces(dtype, dv, T):
+    d, g = scan_inputs(T, (1, T), 2, 1, 64, dv, dtype, rate=0.05)
+    init = randn(g, 1, 2, 64, dv)
+    compare(*run(d, init, None), d, init, None)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of a tensor of more than 2^31 elements: the bits of the dense rows' result."""
+    T, wide = 70000, torch.empty(1, 70000, 32768, dtype=BF16, device="cuda")
+    d, g = scan_inputs(81, (1, T), 2, 1, 128, 64, BF16, wide=False)
+    dense, dfin = run(d, None, None)
+    far = dict(d)
+    at = 32768 - 512
+    for k in ("x", "b", "c"):
+        n = d[k].shape[2] * d[k].shape[3]
+        wide[..., at:at + n] = d[k].flatten(2)
+        far[k] = wide[..., at:at + n].unflatten(-1, d[k].shape[2:])
+        at += n
+    out, fin = run(far, None, None)
+    assert torch.equal(out, dense) and torch.equal(fin, dfin)

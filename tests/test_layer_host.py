@@ -29,7 +29,7 @@ CONV = dict(x=256, ldx=64, weight=512, bias=768, init=1024, out=1280, fin=1536, 
     (dict(bias=772), INVALID), (dict(init=1026), INVALID), (dict(fin=1540), INVALID), (dict(cu=20), INVALID),
     (dict(ldx=63), INVALID), (dict(C=0), INVALID), (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(dt=5), INVALID),
     (dict(act=2), INVALID), (dict(act=9), INVALID), (dict(K=1), UNSUPPORTED), (dict(K=5), UNSUPPORTED),
-    (dict(C=1 << 21, ldx=1 << 21), UNSUPPORTED), (dict(B=4, T=1 << 30), UNSUPPORTED), (dict(T=1 << 33), UNSUPPORTED),
+    (dict(out=256), INVALID), (dict(C=1 << 21, ldx=1 << 21), UNSUPPORTED), (dict(B=4, T=1 << 30), UNSUPPORTED), (dict(T=1 << 33), UNSUPPORTED),
     (dict(B=0), OK),
 ])
 def test_conv_fwd_refusals(kw, code):
