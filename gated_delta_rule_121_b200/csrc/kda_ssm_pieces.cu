@@ -5,65 +5,108 @@
 namespace kda {
 namespace {
 
-constexpr int MAX_PARTS = 64;  // of a sequence of known length (a piece adds up the ones before it)
+constexpr int MAX_PARTS = 64;  // of a sequence of known length
 
-// The pieces of a packed batch, in the sequences' order (one block; entries
-// behind the last one are marked unused).  Running sums of the pieces and of
-// the slots that sequences of several pieces take; offsets that are no
-// offsets may claim more than there is, and what lies beyond is left out.
-// Pieces are twice as long where one sequence holds more than half of the tokens:
-// its pieces alone fill the device then, and a piece adds up the states of all
-// before it (65536 tokens, H = 8, one sequence of 62K: 152 us against 224;
-// 32768 tokens in sequences of up to 10000, H = 48: 358 us against 332 for the
-// short pieces).
+// The pieces of a packed batch (one block): first the ones that others follow,
+// which are whole, then the last ones by length, the longest first, so that blocks
+// that take every so-manyth piece get about the same work; entries behind the last
+// one are marked unused.  Pieces of one length class, and the sequences' slots, come
+// in any order: no result depends on it.  Offsets that are no offsets may claim
+// more than there is, and what lies beyond is left out.
+// Pieces are twice as long where one sequence holds more than half of the tokens: it
+// fills the device with them then.
+constexpr int CLASSES = 64;  // of lengths
 __global__ void __launch_bounds__(1024) ssm_piece_table_kernel(Seqs q, int64_t len, int capacity, int slots,
                                                                PieceEntry* table) {
-  __shared__ int2 part[1024];
-  __shared__ int2 carry;
-  __shared__ int longs;  // sequences of more than half of the tokens
+  __shared__ int place[CLASSES + 1];  // sizes of the classes, then the next free places; 0: pieces that others follow
+  __shared__ int used, total, longs;  // slots, pieces; sequences of more than half of the tokens
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    carry = make_int2(0, 0);
-    longs = 0;
-  }
+  if (tid <= CLASSES) place[tid] = 0;
+  if (tid == 0) used = longs = 0;
   __syncthreads();
   for (int n = tid; n < q.N; n += 1024)
     if (2 * (q.end(n) - q.begin(n)) > q.T) atomicAdd(&longs, 1);
   __syncthreads();
   if (longs) len *= 2;
-  for (int n0 = 0; n0 < q.N; n0 += 1024) {
-    const int n = n0 + tid;
-    int64_t s = 0, e = 0;
-    int cnt = 0;
-    if (n < q.N) {
-      s = q.begin(n);
-      e = max(q.end(n), s);
-      cnt = (int)max((e - s + len - 1) / len, (int64_t)1);
+  auto pieces = [&](int n, int64_t& s, int64_t& e, int& cls) {  // and the class of the last one
+    s = q.begin(n);
+    e = max(q.end(n), s);
+    const int cnt = (int)max((e - s + len - 1) / len, (int64_t)1);
+    cls = CLASSES - (int)((e - s - (cnt - 1) * len) * (CLASSES - 1) / len);
+    return cnt;
+  };
+  int64_t s, e;
+  int cls;
+  for (int n = tid; n < q.N; n += 1024) {
+    const int cnt = pieces(n, s, e, cls);
+    if (cnt > 1) atomicAdd(&place[0], cnt - 1);
+    atomicAdd(&place[cls], 1);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int at = 0;
+    for (int c = 0; c <= CLASSES; ++c) {
+      const int size = place[c];
+      place[c] = at;
+      at += size;
     }
-    const int own = cnt > 1 ? cnt : 0;
-    part[tid] = make_int2(cnt, own);
-    __syncthreads();
-    for (int o = 1; o < 1024; o <<= 1) {
-      const int2 v = tid >= o ? part[tid - o] : make_int2(0, 0);
-      __syncthreads();
-      part[tid].x += v.x;
-      part[tid].y += v.y;
-      __syncthreads();
-    }
-    const int first = carry.x + part[tid].x - cnt, slot0 = carry.y + part[tid].y - own;
+    total = at;
+  }
+  __syncthreads();
+  for (int n = tid; n < q.N; n += 1024) {
+    const int cnt = pieces(n, s, e, cls);
+    const int slot0 = cnt > 1 ? atomicAdd(&used, cnt) : 0, first = cnt > 1 ? atomicAdd(&place[0], cnt - 1) : 0;
+    const int last = atomicAdd(&place[cls], 1), own = cnt > 1 && slot0 + cnt > slots ? -1 : n;
     for (int r = 0; r < cnt; ++r) {
       const int64_t a = s + r * len;
-      if (first + r < capacity)
-        table[first + r] = {slot0 + own <= slots ? n : -1, r, cnt, slot0, (int)a, (int)min(a + len, e), {0, 0}};
+      const int i = r < cnt - 1 ? first + r : last;
+      if (i < capacity) table[i] = {own, r, cnt, slot0, (int)a, (int)min(a + len, e), {0, 0}};
     }
-    __syncthreads();
-    if (tid == 1023) {
-      carry.x += part[1023].x;
-      carry.y += part[1023].y;
-    }
-    __syncthreads();
   }
-  for (int i = carry.x + tid; i < capacity; i += 1024) table[i].n = -1;
+  for (int i = total + tid; i < capacity; i += 1024) table[i].n = -1;
+}
+
+// One sequence's states after each of its parts, in place: S_r = e^{G_r} S_{r-1} + own
+// state of part r.  (Each piece adding up all parts before it read the states again
+// and again: 32 us of a block's 88 for 37 pieces.)  A thread has four elements and
+// loads four parts at once; bound by the latency of that chain, ~4 us for 37 parts.
+constexpr int CT = 128;
+__global__ void __launch_bounds__(CT) ssm_compose_kernel(PieceArgs p, bool init, int H, int size, int blocks) {
+  const int entry = blockIdx.x / blocks, elem = ((blockIdx.x - entry * blocks) * CT + threadIdx.x) * 4;
+  int64_t slot0 = (int64_t)entry * p.per_seq * p.parts;
+  int parts = (p.per_seq - 1) * p.parts;
+  if (p.table) {
+    const PieceEntry e = p.table[entry];
+    if (e.n < 0 || e.r > 0) return;
+    slot0 = e.slot0;
+    parts = e.pieces - 1;
+  }
+  const int seq = H * size;
+  if (elem >= seq) return;
+  float4* o = reinterpret_cast<float4*>(p.state + slot0 * seq + elem);
+  const float* decay = p.decay + slot0 * H + elem / size;
+  const int64_t step = seq / 4;
+  float4 S = init ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int r = 0; r < parts; r += 4) {
+    float4 own[4];
+    float dec[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (r + k >= parts) break;
+      own[k] = o[(r + k + 1) * step];
+      dec[k] = exp2f(decay[(int64_t)(r + k) * H]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (r + k >= parts) break;
+      S.x = fmaf(S.x, dec[k], own[k].x);
+      S.y = fmaf(S.y, dec[k], own[k].y);
+      S.z = fmaf(S.z, dec[k], own[k].z);
+      S.w = fmaf(S.w, dec[k], own[k].w);
+      o[(r + k + 1) * step] = S;
+    }
+  }
 }
 
 }  // namespace
@@ -107,7 +150,7 @@ PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, in
     p.per_seq = p.parts = 1;
     p.len = p.part = len * PIECE_CHUNK;
     p.pieces = N + T / p.len;
-    p.first_pass = T > p.len ? p.pieces : 0;
+    p.first_pass = T > p.len ? T / p.len : 0;  // the pieces that others follow are whole
     // a sequence of L > len tokens has at most L / len + 1 < 2 L / len pieces
     p.slots = p.first_pass ? 2 * T / p.len : 0;
   }
@@ -136,6 +179,13 @@ cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace
   PieceEntry* table = reinterpret_cast<PieceEntry*>(ws + p.table);
   out->table = table;
   ssm_piece_table_kernel<<<1, 1024, 0, s>>>(Seqs{a.cu, a.N, a.T}, p.len, (int)p.pieces, (int)p.slots, table);
+  return cudaGetLastError();
+}
+
+cudaError_t compose_pieces(const PiecePlan& p, const SsmArgs& a, const PieceArgs& pa, cudaStream_t s) {
+  const int size = a.dk * a.dv, blocks = (a.H * size + 4 * CT - 1) / (4 * CT);
+  const int64_t entries = a.cu ? p.first_pass : a.N;  // packed: a sequence's first piece is among the ones that others follow
+  ssm_compose_kernel<<<(unsigned)(entries * blocks), CT, 0, s>>>(pa, a.init != nullptr, a.H, size, blocks);
   return cudaGetLastError();
 }
 

@@ -2,9 +2,10 @@
 // e^{G} S_in + S_own, with G the piece's total log decay and S_own its state from
 // zero, so a sequence can be cut into pieces that run in parallel: a first pass
 // (states only, up to the last piece's start) gives S_own and G of parts of
-// pieces, and a block of the second pass composes its incoming state from the
-// parts before it.  The first pass also keeps the initial state, since the last
-// piece of the second may write the final state over it while others still start.
+// pieces; a running composition turns them into the state at each part's end; the
+// second pass starts a piece from it.  The first pass also keeps the initial state,
+// since the last piece of the second may write the final state over it while others
+// still start.
 #pragma once
 #include "kda_layer.cuh"
 
@@ -14,7 +15,7 @@ constexpr int PIECE_CHUNK = 64;  // pieces are whole chunks of this many tokens
 
 // Tokens [start, end) of sequence n: a piece, or in the first pass a part of one.
 // A sequence of several pieces has slots from slot0 on, for states (the initial
-// one, then the parts') and for the parts' total decays; `before` counts the parts
+// one, then those at the parts' ends) and for the parts' total decays; `before` counts the parts
 // before this one.
 struct Piece {
   int n, slot0, before;
@@ -69,5 +70,7 @@ struct PiecePlan {
 PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, int least, int H, int dk, int dv, bool packed);
 // The pieces' part of a launch's arguments, and for packed batches their table.
 cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace, PieceArgs* out, cudaStream_t s);
+// Between the passes: the parts' own states become the states at their ends.
+cudaError_t compose_pieces(const PiecePlan& p, const SsmArgs& a, const PieceArgs& pa, cudaStream_t s);
 
 }  // namespace kda

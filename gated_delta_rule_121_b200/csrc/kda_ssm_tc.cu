@@ -43,6 +43,8 @@
 // remain.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "kda_ssm_pieces.cuh"
 #include "sm100_ptx.cuh"
 
@@ -95,6 +97,14 @@ enum Bar {
 // each); G_t; G_s - log D_s (both in log2 units).
 constexpr int SC_D = 0, SC_W = 64, SC_CUM = 160, SC_LS = 224;
 
+// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot
+// and head, the log decays that each of the scalars' warps has seen, by head; the
+// block's items.
+constexpr uint32_t MS_TMEM = 488, MS_ABORT = 492, MS_TOTAL = 496, MS_SUM = 544, MS_ITEMS = 560;
+constexpr int MAX_ITEMS = 7;  // of a block
+constexpr uint32_t MISC = MS_ITEMS + MAX_ITEMS * 24;
+static_assert(NUM_BARS * 8 <= MS_TMEM, "barrier area");
+
 template <int DK, int DV, bool STATES>
 struct Cfg {
   static constexpr int HEADS = PT / DV;                  // heads per tile, at most
@@ -111,7 +121,7 @@ struct Cfg {
   static constexpr int DECS = STATES ? 2 : 1;                // warps for the scalars
   static constexpr uint32_t RAW = 4 * HEADS * CH * 4;
   static constexpr uint32_t SM_MISC = SM_RAW + DECS * RAW;
-  static constexpr uint32_t BYTES = SM_MISC + 640 + 1024;
+  static constexpr uint32_t BYTES = SM_MISC + MISC + 1024;
   // TMEM columns; the first pass has room for two of w x and U, so that one is read while the next is made
   static constexpr int NU = STATES ? 2 : 1;
   static constexpr uint32_t TM_WX = 0, TM_S = 128, TM_YI = TM_S + DK / 2, TM_YM = TM_YI + 64,
@@ -121,10 +131,6 @@ struct Cfg {
   static_assert(TM_END <= TM_COLS, "TMEM");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
-// In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot
-// and head, the log decays that each of the scalars' warps has seen, by head.
-constexpr uint32_t MS_TMEM = 512, MS_ABORT = 516, MS_TOTAL = 528, MS_SUM = 576;
-static_assert(NUM_BARS * 8 <= MS_TMEM, "barrier area");
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
@@ -143,6 +149,9 @@ __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap), "r"(src),
                "r"(c0), "r"(c1)
                : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 // 16 lanes x 32 columns (fp32): thread l gets rows l/4 and l/4 + 8, of each 8
 // columns numbers 2 (l % 4) and the next: {r, c}, {r, c+1}, {r+8, c}, {r+8, c+1},
@@ -267,6 +276,8 @@ struct TcArgs {
   SsmArgs a;
   PieceArgs p;
   int hpt, tiles;  // heads per tile, tiles of 128 columns
+  int items;       // pieces times tiles
+  int blocks, per_block;  // of the second pass, and items of a block there
 };
 
 // ------------------------------------------------------------------ roles
@@ -277,9 +288,41 @@ struct TcArgs {
 struct Ctx {
   uint8_t* sm;
   uint32_t sb, tmem, bars;   // shared-window addresses of sm and of the barriers; TMEM base
-  Piece piece;
-  int h0, heads, tile;       // first head of the tile, heads in it
-  int nchunks;
+  int heads;                 // of a tile
+  int items, nchunks;        // of the block
+  const int4* item;          // what the items are (item_index)
+};
+
+// A block's items (a tile of a piece each): one in the first pass; in the second up
+// to MAX_ITEMS, for which the block's start (launch, barriers, TMEM, the first loads)
+// is paid once and the next item's loads and first products run beside the end of
+// the last one (191 packed prompts of up to 200 tokens, H = 16: 94 us, with a block
+// per item 132).  Every gridDim.x-th item in alternating direction, since the table of
+// a packed batch has the long ones first.
+__device__ __forceinline__ int item_index(int turn) {
+  return turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+__device__ __forceinline__ int chunks_of(int tokens) { return (tokens + CH - 1) / CH; }
+// In shared memory, per item: its tokens [tok, end) (none: tok = end), first head and
+// sequence; and its slot0 and 8 before + flags.
+constexpr int SPLIT = 1, LAST = 2, VALID = 4;
+// The chunks of a block's items one after the other; next() is called before the first.
+template <bool ONE>  // one item only, which has chunks
+struct Walk {
+  int turn = 0, tok = 0, end = 0, h0 = 0, n = -1;
+  __device__ __forceinline__ bool next(const Ctx& x) {  // whether it starts an item
+    tok += CH;
+    if (ONE ? turn > 0 : tok < end) return false;
+    tok = end = 0;
+    bool found = false;
+#pragma unroll 1
+    while ((ONE || turn < x.items) && !found) {
+      const int4 d = x.item[turn++];
+      found = d.x < d.y;
+      if (found) tok = d.x, end = d.y, h0 = d.z, n = d.w;
+    }
+    return found;
+  }
 };
 
 // Bounded wait that also gives up once another role has: the first to give up
@@ -327,10 +370,6 @@ __device__ __forceinline__ void commit(const Ctx& x, int bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(x.bars + 8 * bar)
                : "memory");
 }
-__device__ __forceinline__ int valid_rows(const Ctx& x, int i) {
-  const int left = (int)(x.piece.end - x.piece.start) - i * CH;
-  return left < CH ? left : CH;
-}
 // A copy or product in flight has ended, whatever else the block gave up.
 __device__ __forceinline__ void land(uint32_t bar, uint32_t parity) {
   asm volatile(
@@ -365,57 +404,61 @@ template <int DK, int DV, bool STATES>
 __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const void* tx, const void* tb, const void* tc,
                                           const void* to, bool leader) {
   using K = Cfg<DK, DV, STATES>;
-  const int atoms = x.heads * DV / 64, group = x.h0 / (t.a.H / t.a.G), col = x.h0 * DV, tok0 = (int)x.piece.start;
+  const int atoms = x.heads * DV / 64, per_group = t.a.H / t.a.G;
   int nk = 0, nx = 0;  // chunks whose loads have been issued
+  Walk<STATES> wk, wx, wo;     // chunks to load next (b and c; x), and to store
   Ring<K::NB> k;
   Ring<K::NX> s;
   auto load_k = [&]() {
+    wk.next(x);
     if (leader) {
       const uint32_t bar = x.bars + 8 * (B_KFULL + k.st), dst = x.sb + K::SM_K + k.st * K::K_BYTES;
+      const int col = wk.h0 / per_group * DK;
       expect_tx(bar, K::K_BYTES);
 #pragma unroll
       for (int e = 0; e < DK / 64; ++e) {
-        tma_load_2d(dst + e * 8192, tb, bar, group * DK + 64 * e, tok0 + nk * CH);
-        if (!STATES) tma_load_2d(dst + K::KV + e * 8192, tc, bar, group * DK + 64 * e, tok0 + nk * CH);
+        tma_load_2d(dst + e * 8192, tb, bar, col + 64 * e, wk.tok);
+        if (!STATES) tma_load_2d(dst + K::KV + e * 8192, tc, bar, col + 64 * e, wk.tok);
       }
     }
     ++nk;
     k.next();
   };
   auto load_x = [&]() {
+    const bool fresh = wx.next(x);
     if (leader) {
       const uint32_t bar = x.bars + 8 * (B_XFULL + s.st), dst = x.sb + K::SM_X + s.st * K::X_BYTES;
       expect_tx(bar, atoms * 8192);
-      tma_load_2d(dst, tx, bar, col, tok0 + nx * CH);
-      if (atoms == 2) tma_load_2d(dst + 8192, tx, bar, col + 64, tok0 + nx * CH);
+      tma_load_2d(dst, tx, bar, wx.h0 * DV, wx.tok);
+      if (atoms == 2) tma_load_2d(dst + 8192, tx, bar, wx.h0 * DV + 64, wx.tok);
     }
     ++nx;
     s.next();
+    if (fresh && leader && nx > 1 && t.a.init) {  // the item's initial state into L2
+      const float* o = t.a.init + ((int64_t)wx.n * t.a.H + wx.h0) * DK * DV;
+      for (int h = 0; h < x.heads; ++h) prefetch_l2(o + h * DK * DV, DK * DV * 4);
+    }
   };
 #pragma unroll 1
-  while (nx < K::NX && nx < x.nchunks) {
-    if (nk < K::NB) load_k();
-    load_x();
-  }
-#pragma unroll 1
-  for (int i = 0; i < x.nchunks; ++i) {
-    if (leader && i + K::NX + 1 < x.nchunks) {  // into L2, a chunk before its load
-      for (int e = 0; e < atoms; ++e) tma_prefetch_2d(tx, col + 64 * e, tok0 + (i + K::NX + 1) * CH);
+  for (int i = -K::NX; i < x.nchunks; ++i) {  // chunk i's store; the loads run ahead
+    if (leader && i >= 0 && wx.tok + 2 * CH < wx.end) {  // into L2, a chunk before its load
+      for (int e = 0; e < atoms; ++e) tma_prefetch_2d(tx, wx.h0 * DV + 64 * e, wx.tok + 2 * CH);
     }
-    if (i + K::NB < x.nchunks) {  // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
-      if (!wait_bar(x, B_KFREE + k.st, k.ph ^ 1)) break;
+    if (i + K::NB >= 0 && i + K::NB < x.nchunks) {  // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
+      if (i >= 0 && !wait_bar(x, B_KFREE + k.st, k.ph ^ 1)) break;
       load_k();
     }
-    if (!STATES) {
+    if (!STATES && i >= 0) {
+      wo.next(x);
       const int st = i % K::NX;
       if (!wait_bar(x, B_YOUT + st, (i / K::NX) & 1)) break;
       __syncwarp();
-      const int v = valid_rows(x, i);
+      const int v = min(wo.end - wo.tok, CH), col = wo.h0 * DV;
       const uint32_t at = K::SM_X + st * K::X_BYTES;
       if (v == CH) {
         if (leader) {
-          tma_store_2d(to, x.sb + at, col, tok0 + i * CH);
-          if (atoms == 2) tma_store_2d(to, x.sb + at + 8192, col + 64, tok0 + i * CH);
+          tma_store_2d(to, x.sb + at, col, wo.tok);
+          if (atoms == 2) tma_store_2d(to, x.sb + at + 8192, col + 64, wo.tok);
           bulk_commit();
           if (i + K::NX < x.nchunks) bulk_wait_read0();
         }
@@ -425,12 +468,13 @@ __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const v
         for (int e = threadIdx.x & 31; e < atoms * v * 8; e += 32) {
           const int atom = e / (v * 8), r = (e - atom * v * 8) >> 3, c = e & 7;
           const uint4 u = *reinterpret_cast<const uint4*>(x.sm + at + atom * 8192 + r * 128 + ((c ^ (r & 7)) << 4));
-          *reinterpret_cast<uint4*>(out + ((int64_t)tok0 + i * CH + r) * ((int64_t)t.a.H * DV) + atom * 64 + c * 8) = u;
+          *reinterpret_cast<uint4*>(out + ((int64_t)wo.tok + r) * ((int64_t)t.a.H * DV) + atom * 64 + c * 8) = u;
         }
+        fence_proxy_async_smem();  // read before the next load into this stage
       }
     }
     if (i + K::NX < x.nchunks) {
-      if (STATES && !wait_bar(x, B_XFREE + s.st, s.ph ^ 1)) break;
+      if (STATES && i >= 0 && !wait_bar(x, B_XFREE + s.st, s.ph ^ 1)) break;
       __syncwarp();
       load_x();
     }
@@ -569,18 +613,22 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
   const int lane = threadIdx.x & 31, l = lane & 15;
   const int h = x.heads == 2 ? lane >> 4 : 0;
   const bool writes = (lane >> 4) == h;
-  const float rate = -expf(a.A_log[x.h0 + h]) * LOG2E;
+  Walk<STATES> wf, wp;  // chunks to fetch delta of, and to make the scalars of
+  float rate = 0.f, bias = 0.f;
   const bool soft = a.dt_bias != nullptr;
   float total = 0.f;
   const int sh = x.heads - 1, per = 32 >> sh, tok = lane >> sh;  // tokens per 32 elements; this lane's first
-  const float bias = soft ? a.dt_bias[x.h0 + (lane & sh)] : 0.f;
   const int64_t step = (int64_t)per * a.H;
-  const float* src = a.delta + (x.piece.start + which * CH + tok) * a.H + x.h0 + (lane & sh);
-  int left = (int)(x.piece.end - x.piece.start) - which * CH - tok;  // of the tokens from this lane's first one in the next fetch
+  if (which) {
+    wf.next(x);
+    wp.next(x);
+  }
   uint32_t dst = 0;
   const uint32_t raw0 = x.sb + K::SM_RAW + which * K::RAW + lane * 4;
   auto fetch = [&]() {
-    const float* p = src;
+    wf.next(x);
+    const float* p = a.delta + (int64_t)(wf.tok + tok) * a.H + wf.h0 + (lane & sh);
+    const int left = wf.end - wf.tok - tok;  // tokens from this lane's first one on (none behind the last chunk)
 #pragma unroll
     for (int k = 0; k < E; ++k, p += step) {
       if (k * per < CH) {
@@ -591,8 +639,7 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    src += (int64_t)K::DECS * CH * a.H;
-    left -= K::DECS * CH;
+    if (K::DECS == 2) wf.next(x);
     dst = (dst + K::HEADS * CH * 4) & (4 * K::HEADS * CH * 4 - 1);
   };
   const float* raw = reinterpret_cast<const float*>(x.sm + K::SM_RAW + which * K::RAW) + lane;
@@ -607,7 +654,11 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
     fetch();       // three of its chunks ahead
     if (m < 0) continue;
     const int i = m * K::DECS + which;
-    const int v = valid_rows(x, i);
+    if (wp.next(x) || m == 0) {  // a new item
+      rate = -expf(a.A_log[wp.h0 + h]) * LOG2E;
+      bias = soft ? a.dt_bias[wp.h0 + (lane & sh)] : 0.f;
+    }
+    const int v = min(wp.end - wp.tok, CH);
     asm volatile("cp.async.wait_group 3;" ::: "memory");
     __syncwarp();
     float d[E];
@@ -661,6 +712,7 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
     }
     __syncwarp();
     if (lane == 0) arrive(x, B_DEC + s.st);
+    if (K::DECS == 2) wp.next(x);
     s.next();
     if (K::DECS == 2) s.next();
   }
@@ -686,13 +738,15 @@ __device__ __forceinline__ void role_wx(const Ctx& x, int tb0, int tb1) {
   const int row = ((lane >> 4) & 1) * 8 + (lane & 7), ch = (wq & 1) * 4 + ((lane >> 3) & 1);
   const uint32_t xl = x.sb + K::SM_X + (wq >> 1) * 8192 + row * 128;
   const uint32_t sw0 = (uint32_t)(ch ^ (row & 7)) << 4, sw1 = (uint32_t)((ch + 2) ^ (row & 7)) << 4;
+  Walk<STATES> wv;
   Ring<K::NX> s;
   Ring<K::NB> kr;
 #pragma unroll 1
   for (int i = 0; i < x.nchunks; ++i, s.next(), kr.next()) {
     wait_bar(x, B_DEC + s.st, s.ph);
     wait_bar(x, B_XFULL + s.st, s.ph);
-    const int v = valid_rows(x, i);
+    if (!STATES) wv.next(x);
+    const int v = wv.end - wv.tok;
     if (!STATES && v < CH) {  // (the first pass's parts are whole chunks)
       // Rows behind the sequence's end hold other data: x and b become zero,
       // so that nothing of them (an infinity among it) reaches a product.
@@ -834,53 +888,70 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
   const int hl = DV == 64 ? p / 64 : 0;
   const bool live = hl < x.heads;
   const int head = live ? hl : 0, hl_sc = head * K::SC_FLOATS;
-  const int64_t at = ((int64_t)x.h0 + head) * DK * DV + (p & (DV - 1)) + (int64_t)n0 * DV, seq = (int64_t)a.H * DK * DV;
+  const int64_t at0 = (p & (DV - 1)) + (int64_t)n0 * DV, seq = (int64_t)a.H * DK * DV;
   float S[NC];
+  // at: this thread's elements in a sequence's states
+  auto start = [&](int sequence, int slot0, int flags, int64_t at) {  // the state before an item
+    const int before = flags >> 3;
 #pragma unroll
-  for (int n = 0; n < NC; ++n) S[n] = 0.f;
-  float* slots = t.p.state + at;  // slot s of this thread's elements at slots + s * seq
-  const int64_t s0 = x.piece.slot0;
-  if (!STATES && live && x.piece.split) {
-    // the state before this piece, from the parts before it; a few elements and
-    // several parts at a time, so that the loads overlap
+    for (int n = 0; n < NC; ++n) S[n] = 0.f;
+    float* slots = t.p.state + at;  // slot s of this thread's elements at slots + s * seq
+    const int64_t s0 = slot0;
+    const bool cut = !STATES && (flags & SPLIT);  // the first pass left it then
+    if (live && (cut ? a.init || before > 0 : a.init && (!STATES || before == 0))) {
+      const float* o = cut ? slots + (s0 + before) * seq : a.init + sequence * seq + at;
 #pragma unroll
-    for (int g = 0; g < NC; g += 8) {
-      if (a.init) {
+      for (int n = 0; n < NC; ++n) S[n] = o[(int64_t)n * DV];
+      if (STATES) {  // kept for the second pass
 #pragma unroll
-        for (int n = 0; n < 8; ++n) S[g + n] = slots[s0 * seq + (int64_t)(g + n) * DV];
-      }
-#pragma unroll 2
-      for (int r = 0; r < x.piece.before; ++r) {
-        const float dec = ex2(t.p.decay[(s0 + r) * a.H + x.h0 + head]);
-        const float* o = slots + (s0 + r + 1) * seq + (int64_t)g * DV;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) S[g + n] = fmaf(S[g + n], dec, o[(int64_t)n * DV]);
-      }
-    }
-  } else if (live && a.init && (!STATES || x.piece.first)) {
-    const float* o = a.init + x.piece.n * seq + at;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) S[n] = o[(int64_t)n * DV];
-    if (STATES) {  // kept for the second pass
-#pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        slots[s0 * seq + (int64_t)n * DV] = S[n];
-        S[n] = 0.f;
+        for (int n = 0; n < NC; ++n) {
+          slots[s0 * seq + (int64_t)n * DV] = S[n];
+          S[n] = 0.f;
+        }
       }
     }
-  }
+  };
+  auto finish = [&](int sequence, int slot0, int flags, int64_t at) {  // the state after an item
+    float* o = nullptr;
+    if (STATES)
+      o = t.p.state + at + ((int64_t)slot0 + (flags >> 3) + 1) * seq;
+    else if (a.fin && (flags & LAST))
+      o = a.fin + sequence * seq + at;
+    if (live && o) {
+#pragma unroll
+      for (int n = 0; n < NC; ++n) o[(int64_t)n * DV] = S[n];
+    }
+  };
   const float* totals = reinterpret_cast<const float*>(x.sm + K::SM_MISC + MS_TOTAL) + head;
   // outputs: this warp has tokens 16 part .. 16 part + 15 of value columns 32 q .. 32 q + 31
   const int q = w & 3, part = w >> 2;
-  const float skip = !STATES && a.D ? a.D[x.h0 + head] : 0.f;
-  const float2 skip2 = make_float2(skip, skip);
+  float skip = 0.f, skip_now = 0.f;  // D of the chunk before, and of this one
   const int row = 16 * part + ((lane >> 4) & 1) * 8 + (lane & 7), ch = (q & 1) * 4 + ((lane >> 3) & 1);
   const uint32_t xl = x.sb + K::SM_X + (q >> 1) * 8192 + row * 128;
   const uint32_t sw0 = (uint32_t)(ch ^ (row & 7)) << 4, sw1 = (uint32_t)((ch + 2) ^ (row & 7)) << 4;
   Ring<K::NX> s, so;  // stages of the chunk, and of the one before it
+  int turn = -1, left = 0;  // this item's turn, its chunks left
 #pragma unroll 1
-  for (int i = 0; STATES ? i < x.nchunks : i <= x.nchunks; ++i) {
-    if (!STATES && i < x.nchunks) {  // S before the chunk as bf16 pairs: the A operand of YI
+  for (int i = 0;; ++i) {
+#pragma unroll 1
+    for (int begin = 0; left == 0 && turn < x.items; begin ^= 1) {  // the end of an item, and the next one's start
+      if (begin && ++turn == x.items) break;
+      if (turn < 0) continue;
+      const int4 d = x.item[turn];
+      const int2 f = reinterpret_cast<const int2*>(x.item + MAX_ITEMS)[turn];
+      if (!(f.y & VALID)) continue;
+      const int hh = d.z + head;
+      const int64_t at = (int64_t)hh * DK * DV + at0;
+      if (begin) {
+        left = chunks_of(d.y - d.x);
+        if (!STATES && a.D) skip_now = a.D[hh];
+        start(d.w, f.x, f.y, at);
+      } else {
+        finish(d.w, f.x, f.y, at);
+      }
+    }
+    const bool more = turn < x.items;  // whether there is a chunk i
+    if (!STATES && more) {  // S before the chunk as bf16 pairs: the A operand of YI
       if (i > 0) wait_bar(x, B_SFREE, (i - 1) & 1);
       __syncwarp();
       tc_fence_after();
@@ -918,7 +989,7 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float2 y = __ffma2_rn(f[j >> 1], make_float2(yi[2 * j], yi[2 * j + 1]), make_float2(ym[2 * j], ym[2 * j + 1]));
-          y = __ffma2_rn(skip2, bf16x2_f32(raw[j]), y);
+          y = __ffma2_rn(make_float2(skip, skip), bf16x2_f32(raw[j]), y);
           pk[j] = pack_bf16x2(y.x, y.y);
         }
         stsm_x4_t(xe, pk);
@@ -927,7 +998,10 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
       arrive(x, B_YOUT + so.st);  // (and the stage's scalars have been read)
       so.next();
     }
-    if (i < x.nchunks) {  // S after the chunk
+    if (!more) break;
+    skip = skip_now;
+    --left;
+    {  // S after the chunk
       wait_bar(x, B_U + 2 * (i & 1) + 1, (i >> 1) & 1);  // (made from this chunk's scalars)
       __syncwarp();
       tc_fence_after();
@@ -953,16 +1027,6 @@ __device__ __forceinline__ void role_state(const Ctx& x, const TcArgs& t) {
       s.next();
     }
   }
-  if (!live) return;
-  float* o = nullptr;
-  if (STATES)
-    o = slots + (s0 + x.piece.before + 1) * seq;
-  else if (a.fin && x.piece.last)
-    o = a.fin + x.piece.n * seq + at;
-  if (o) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n) o[(int64_t)n * DV] = S[n];
-  }
 }
 
 template <int DK, int DV, bool STATES>
@@ -973,14 +1037,12 @@ __global__ void __launch_bounds__(NTHR, 1)
   using K = Cfg<DK, DV, STATES>;
   extern __shared__ uint8_t smem_raw[];
   Ctx x;
-  x.tile = blockIdx.x % t.tiles;
-  if (!find_piece<STATES>(t.p, t.a.T, blockIdx.x / t.tiles, x.piece)) return;
+  Piece piece;
+  if (STATES && !find_piece<true>(t.p, t.a.T, blockIdx.x / t.tiles, piece)) return;
   x.sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   x.sb = smem_u32(x.sm);
   x.bars = x.sb + K::SM_MISC;
   x.heads = t.hpt;
-  x.h0 = x.tile * t.hpt;
-  x.nchunks = ((int)(x.piece.end - x.piece.start) + CH - 1) / CH;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   uint8_t* misc = x.sm + K::SM_MISC;
   if (tid < NUM_BARS) {
@@ -1002,6 +1064,20 @@ __global__ void __launch_bounds__(NTHR, 1)
     prefetch_tmap(&tc);
     prefetch_tmap(&to);
   }
+  int4* item = reinterpret_cast<int4*>(misc + MS_ITEMS);
+  x.item = item;
+  x.items = STATES ? 1 : t.per_block;
+  if (tid >= 64 && tid < 64 + x.items) {
+    const int index = item_index(tid - 64);
+    int4 d = make_int4(0, 0, 0, 0);
+    int2 s = make_int2(0, 0);
+    if (STATES || (index < t.items && find_piece<STATES>(t.p, t.a.T, index / t.tiles, piece))) {
+      d = make_int4((int)piece.start, (int)piece.end, index % t.tiles * t.hpt, piece.n);
+      s = make_int2(piece.slot0, piece.before * 8 + VALID + (piece.last ? LAST : 0) + (piece.split ? SPLIT : 0));
+    }
+    item[tid - 64] = d;
+    reinterpret_cast<int2*>(item + MAX_ITEMS)[tid - 64] = s;
+  }
   if (!STATES) {  // zero tiles and score tiles
     for (int e = tid; e < (int)(K::ZERO / 16); e += NTHR) {
       reinterpret_cast<uint4*>(x.sm + K::SM_Z0)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -1018,6 +1094,11 @@ __global__ void __launch_bounds__(NTHR, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  x.nchunks = 0;
+  for (int k = 0; k < x.items; ++k) {
+    const int4 d = x.item[k];
+    x.nchunks += chunks_of(d.y - d.x);
+  }
   x.tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(misc + MS_TMEM), 0);
 
   if (warp >= W_MOVE) {
@@ -1048,7 +1129,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   __syncthreads();
   if (STATES && tid < x.heads) {
     const float* sum = reinterpret_cast<const float*>(misc + MS_SUM) + tid;
-    t.p.decay[(int64_t)(x.piece.slot0 + x.piece.before) * t.a.H + x.h0 + tid] = sum[0] + sum[2];
+    t.p.decay[(int64_t)(piece.slot0 + piece.before) * t.a.H + blockIdx.x % t.tiles * t.hpt + tid] = sum[0] + sum[2];
   }
   if (tid == 0 && *reinterpret_cast<volatile int*>(misc + MS_ABORT) != 0) record_error(t.a.status, KDA_ERR_TIMEOUT, 1);
   if (warp == 0) {
@@ -1087,12 +1168,14 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t width, int64_t ld, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int PLACES = 148;  // blocks at a time, one per SM
+
 // Heads per tile.
 int heads_per_tile(int H, int G, int dv) { return dv == 64 && (H / G) % 2 == 0 ? 2 : 1; }
 
 PiecePlan plan(int N, int64_t T, int H, int G, int dk, int dv, bool packed) {
   // one block per SM; a chunk of the first pass takes about 0.4 of one of the second
-  return plan_pieces(N, T, H / heads_per_tile(H, G, dv), 148, 0.4, 4, H, dk, dv, packed);
+  return plan_pieces(N, T, H / heads_per_tile(H, G, dv), PLACES, 0.4, 4, H, dk, dv, packed);
 }
 
 template <int DK, int DV, bool STATES>
@@ -1114,9 +1197,10 @@ cudaError_t launch(const TcArgs& t, const PiecePlan& p, cudaStream_t s) {
   if (p.first_pass) {
     if ((e = ready<DK, DV, true>()) != cudaSuccess) return e;
     ssm_tc_kernel<DK, DV, true><<<(unsigned)(p.first_pass * t.tiles), NTHR, Cfg<DK, DV, true>::BYTES, s>>>(tx, tb, tc, to, t);
+    if ((e = compose_pieces(p, a, t.p, s)) != cudaSuccess) return e;
   }
   if ((e = ready<DK, DV, false>()) != cudaSuccess) return e;
-  ssm_tc_kernel<DK, DV, false><<<(unsigned)(p.pieces * t.tiles), NTHR, Cfg<DK, DV, false>::BYTES, s>>>(tx, tb, tc, to, t);
+  ssm_tc_kernel<DK, DV, false><<<(unsigned)t.blocks, NTHR, Cfg<DK, DV, false>::BYTES, s>>>(tx, tb, tc, to, t);
   return cudaGetLastError();
 }
 
@@ -1134,6 +1218,12 @@ cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s)
   t.a = a;
   t.hpt = heads_per_tile(a.H, a.G, a.dv);
   t.tiles = a.H / t.hpt;
+  t.items = (int)(p.pieces * t.tiles);
+  // as many blocks as the device holds, or a multiple of that where they would have
+  // too many items; all with the same number of items where that is known here
+  t.blocks = std::min(t.items, (t.items + PLACES * MAX_ITEMS - 1) / (PLACES * MAX_ITEMS) * PLACES);
+  t.per_block = (t.items + t.blocks - 1) / t.blocks;
+  if (!a.cu) t.blocks = (t.items + t.per_block - 1) / t.per_block;
   cudaError_t e = prepare_pieces(p, a, workspace, &t.p, s);
   if (e != cudaSuccess) return e;
   if (a.dk == 128) return a.dv == 128 ? launch<128, 128>(t, p, s) : launch<128, 64>(t, p, s);
