@@ -316,7 +316,7 @@ struct Walk {
     tok = end = 0;
     bool found = false;
 #pragma unroll 1
-    while ((ONE || turn < x.items) && !found) {
+    while (turn < x.items && !found) {
       const int4 d = x.item[turn++];
       found = d.x < d.y;
       if (found) tok = d.x, end = d.y, h0 = d.z, n = d.w;
@@ -444,7 +444,8 @@ __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const v
     if (leader && i >= 0 && wx.tok + 2 * CH < wx.end) {  // into L2, a chunk before its load
       for (int e = 0; e < atoms; ++e) tma_prefetch_2d(tx, wx.h0 * DV + 64 * e, wx.tok + 2 * CH);
     }
-    if (i + K::NB >= 0 && i + K::NB < x.nchunks) {  // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
+    // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
+    if (i + K::NB >= 0 && i + K::NB < x.nchunks) {
       if (i >= 0 && !wait_bar(x, B_KFREE + k.st, k.ph ^ 1)) break;
       load_k();
     }

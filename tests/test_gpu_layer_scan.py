@@ -241,3 +241,41 @@ def test_offsets_beyond_32_bits():
         at += n
     out, fin = run(far, None, None)
     assert torch.equal(out, dense) and torch.equal(fin, dfin)
+
+
+@pytest.mark.parametrize("dv,H,G", [(64, 2, 1), (128, 2, 2)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_sequences(dv, H, G, in_place):
+    """More sequences than blocks, so that a block goes from one to the next: empty
+    ones, single tokens and odd lengths among them."""
+    lengths = [(7 * i * i + 3) % 83 if i % 11 else 0 for i in range(210)]
+    d, g = scan_inputs(51, (1, sum(lengths)), H, G, 64, dv, BF16)
+    cu = offsets(lengths)
+    init = randn(g, len(lengths), H, 64, dv)
+    state = init.clone()
+    out, fin = run(d, state, cu, final_state=state if in_place else None)
+    compare(out, fin, d, init, cu)
+
+
+def test_many_short_sequences():
+    """More items than blocks take in one wave."""
+    d, g = scan_inputs(52, (1100, 3), 1, 1, 64, 64, BF16)
+    init = randn(g, 1100, 1, 64, 64)
+    compare(*run(d, init, None), d, init, None)
+
+
+def test_spoilt_sequences_among_many():
+    """A block that goes on after a sequence with NaN and infinities carries nothing over."""
+    lengths = [64, 65, 3] * 80
+    d, g = scan_inputs(53, (1, sum(lengths)), 2, 1, 64, 64, BF16)
+    cu = offsets(lengths)
+    init = randn(g, len(lengths), 2, 64, 64)
+    ok_out, ok_fin = run(d, init, cu)
+    bad = torch.zeros(len(lengths), dtype=torch.bool)
+    bad[::4] = True
+    rows = torch.repeat_interleave(bad, torch.tensor(lengths)).cuda()
+    for k, v in (("x", float("nan")), ("b", float("inf")), ("c", float("-inf")), ("delta", float("nan"))):
+        d[k][0, rows] = v
+    out, fin = run(d, init, cu)
+    assert torch.equal(out[0, ~rows], ok_out[0, ~rows])
+    assert torch.equal(fin[~bad.cuda()], ok_fin[~bad.cuda()])
