@@ -7,8 +7,9 @@
 // group in registers, takes the mean and then the mean of the centred squares
 // (two passes over registers, so no cancellation), and writes the result.  HBM
 // bandwidth bounds it: 6 bytes per bf16 element with a gate, 4 without.
-// Measured: 64K rows of 96 groups of 128, bf16 with a gate, 0.72 ms, 6.7 TB/s, a
-// copy's rate; 512 rows of one group of 6144 8 us, most of it the launch.
+// Measured: 64K rows of 96 groups of 128, bf16 with a gate, 0.71 to 0.81 ms (by where
+// the buffers lie), 6.0 to 6.8 TB/s, a copy's rate; 512 rows of one group of 6144 8
+// us, most of it the launch.
 #include "kda_layer.cuh"
 
 namespace kda {

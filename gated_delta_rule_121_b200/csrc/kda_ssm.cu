@@ -17,7 +17,7 @@
 // token (over thousands of slowly decaying tokens those add up to 1e-6).  Where
 // a stage decays by more than 2^-20 the plain recurrence runs instead.
 //   The column's chain of multiply-adds bounds it (4 dk dv flops per token and
-// head): fp32, 2 x 1000 tokens, 4 heads, 16 x 16 states, 35 us.
+// head): fp32, 2 x 1000 tokens, 4 heads, 16 x 16 states, 33 us.
 //
 // Single token: as the KDA decode step, the state is streamed once through
 // registers; HBM bandwidth bounds it (8 dk dv bytes per head): 512

@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(1024) ssm_piece_table_kernel(Seqs q, int64_t l
 // loads four parts at once; bound by the latency of that chain, ~4 us for 37 parts.
 constexpr int CT = 128;
 __global__ void __launch_bounds__(CT) ssm_compose_kernel(PieceArgs p, bool init, int H, int size, int blocks) {
+  start_next();
+  await_last();
   const int entry = blockIdx.x / blocks, elem = ((blockIdx.x - entry * blocks) * CT + threadIdx.x) * 4;
   int64_t slot0 = (int64_t)entry * p.per_seq * p.parts;
   int parts = (p.per_seq - 1) * p.parts;
@@ -185,8 +187,8 @@ cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace
 cudaError_t compose_pieces(const PiecePlan& p, const SsmArgs& a, const PieceArgs& pa, cudaStream_t s) {
   const int size = a.dk * a.dv, blocks = (a.H * size + 4 * CT - 1) / (4 * CT);
   const int64_t entries = a.cu ? p.first_pass : a.N;  // packed: a sequence's first piece is among the ones that others follow
-  ssm_compose_kernel<<<(unsigned)(entries * blocks), CT, 0, s>>>(pa, a.init != nullptr, a.H, size, blocks);
-  return cudaGetLastError();
+  return launch_overlapped(ssm_compose_kernel, (unsigned)(entries * blocks), CT, 0, s, pa, a.init != nullptr, a.H, size,
+                           blocks);
 }
 
 }  // namespace kda

@@ -70,6 +70,27 @@ struct PiecePlan {
 PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, int least, int H, int dk, int dv, bool packed);
 // The pieces' part of a launch's arguments, and for packed batches their table.
 cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace, PieceArgs* out, cudaStream_t s);
+// The launches from the first pass on overlap: a kernel lets the next one's blocks
+// start as soon as all of its own have (start_next), and that one waits for the
+// kernel before it to end, with all its writes, before it touches what they share
+// (await_last).  A launch, a block's barriers and TMEM are ready by then.
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), unsigned blocks, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Between the passes: the parts' own states become the states at their ends.
 cudaError_t compose_pieces(const PiecePlan& p, const SsmArgs& a, const PieceArgs& pa, cudaStream_t s);
 

@@ -34,9 +34,10 @@
 //
 // Long sequences are cut into pieces that run in parallel (kda_ssm_pieces.cuh).
 //
-// Measured, 64K tokens, 96 heads, dk = 128, dv = 64 (48 tiles, three pieces): 0.88
-// ms, of which 0.22 the first pass (0.95 us a chunk) and 0.66 the second (1.95 us
-// a chunk).  The second pass is bound by the instructions around its products:
+// Measured, 64K tokens, 96 heads, dk = 128, dv = 64 (48 tiles, three pieces): 0.91
+// ms on the same buffers again and again, of which 0.22 the first pass (0.95 us a
+// chunk) and 0.68 the second (2 us a chunk); 1.07 with other inputs in between.
+// The second pass is bound by the instructions around its products:
 // issue slots 64 % busy, the shared-memory pipe ~80 % (the roles' accesses and the
 // operands'), the tensor pipe 54 %, DRAM 31 %.  A state of 64 columns per thread
 // in eight warps (fewer instructions in all) does not fit the registers that
@@ -1038,6 +1039,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   using K = Cfg<DK, DV, STATES>;
   extern __shared__ uint8_t smem_raw[];
   Ctx x;
+  if (STATES) start_next();
   Piece piece;
   if (STATES && !find_piece<true>(t.p, t.a.T, blockIdx.x / t.tiles, piece)) return;
   x.sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1092,6 +1094,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     tmem_alloc(reinterpret_cast<uint32_t*>(misc + MS_TMEM), K::TM_COLS);
     tmem_relinquish();
   }
+  if (!STATES) await_last();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1201,7 +1204,9 @@ cudaError_t launch(const TcArgs& t, const PiecePlan& p, cudaStream_t s) {
     if ((e = compose_pieces(p, a, t.p, s)) != cudaSuccess) return e;
   }
   if ((e = ready<DK, DV, false>()) != cudaSuccess) return e;
-  ssm_tc_kernel<DK, DV, false><<<(unsigned)t.blocks, NTHR, Cfg<DK, DV, false>::BYTES, s>>>(tx, tb, tc, to, t);
+  constexpr int bytes = Cfg<DK, DV, false>::BYTES;
+  if (p.first_pass) return launch_overlapped(ssm_tc_kernel<DK, DV, false>, t.blocks, NTHR, bytes, s, tx, tb, tc, to, t);
+  ssm_tc_kernel<DK, DV, false><<<(unsigned)t.blocks, NTHR, bytes, s>>>(tx, tb, tc, to, t);
   return cudaGetLastError();
 }
 

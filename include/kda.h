@@ -561,7 +561,7 @@ KDA_API kda_status_t kda_group_norm(const void *x, int64_t ldx, const void *gate
                                     int gate_first, void *stream, kda_dtype_t dt);
 
 /*
- * Read back the device status word of a workspace used by kda_fwd.
+ * Read back the device status word of a workspace used by kda_fwd or kda_ssm_fwd.
  * Synchronises `stream` (it is the one call that does) and returns KDA_OK or
  * the first device-side error recorded since the workspace was last passed
  * to kda_fwd (KDA_ERR_TIMEOUT when a bounded wait expired, KDA_ERR_RANGE
