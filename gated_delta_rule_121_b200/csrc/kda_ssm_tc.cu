@@ -8,6 +8,16 @@
 //   S   <- e^{G_C} S + sum_s b_s (e^{G_C - G_s} D_s x_s)^T
 // No exponent is positive, whatever the decays.
 //
+// The scores' exponents.  A difference of two sums over the whole chunk keeps only
+// what the sums' size leaves of it (sums of 1e6: 6 %), so they are made from sums
+// over 16 tokens: for tokens of one sixteen the difference of their sums to its
+// end; else the sum from behind s to the end of its sixteen, the whole sixteens
+// between, and from the start of t's sixteen to t.  A token's log decay counts as
+// MIN_LOG2 where it is below that: a score across such a token is zero in fp32
+// either way, for the largest D_s as well, and the sums stay within 4096, so that an
+// exponent is off by 2^-10 at most: 0.07 % of the score, of which half a bf16 step
+// is 0.4 %.
+//
 // A block walks one piece of a sequence for one tile of 128 value columns: a
 // head of dv = 128, or two heads of dv = 64 that read the same b and c (one
 // head and 64 idle columns where a group has an odd number of heads).  All
@@ -93,10 +103,14 @@ enum Bar {
   NUM_BARS
 };
 
-// Scalars of a chunk, per head, at these 32-bit words: the steps D_s; the
+// Scalars of a chunk, per head, at these 32-bit words: the steps D_s, and in their
+// place DOWN_s + log2 D_s (the scores' columns); the
 // weights w_s = e^{G_C - G_s} D_s as three bf16 terms (pairs of tokens, 32 words
-// each); G_t; G_s - log D_s (both in log2 units).
-constexpr int SC_D = 0, SC_W = 64, SC_CUM = 160, SC_LS = 224;
+// each); G_t; and DOWN, the sums of log decays from behind a token to the end of
+// its sixteen (zero for the last one, in whose place the sixteen's total stands): both
+// in log2 units.
+constexpr int SC_D = 0, SC_COL = 0, SC_W = 64, SC_CUM = 160, SC_DOWN = 224;
+constexpr float MIN_LOG2 = -256.f;  // of a token's decay
 
 // In SM_MISC, behind the barriers: TMEM address, abort flag, totals e^{G_C} by slot
 // and head, the log decays that each of the scalars' warps has seen, by head; the
@@ -255,6 +269,12 @@ __device__ __forceinline__ uint32_t upper_halves(float2 v) {
 __device__ __forceinline__ float2 below_upper(float2 v) {  // what that leaves, exactly
   return make_float2(v.x - __uint_as_float(__float_as_uint(v.x) & 0xffff0000u),
                      v.y - __uint_as_float(__float_as_uint(v.y) & 0xffff0000u));
+}
+// max(a, b), and what is not a number stays so.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 // Packed bf16 arithmetic, rounded to nearest.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -678,7 +698,8 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
     __syncwarp();
     float* o = out + slot;
     const float4 d4 = *reinterpret_cast<const float4*>(o + SC_D);
-    const float g0 = rate * d4.x, g1 = rate * d4.y, g2 = rate * d4.z, g3 = rate * d4.w;
+    const float g0 = max_nan(rate * d4.x, MIN_LOG2), g1 = max_nan(rate * d4.y, MIN_LOG2);
+    const float g2 = max_nan(rate * d4.z, MIN_LOG2), g3 = max_nan(rate * d4.w, MIN_LOG2);
     // sums up to each token, and from behind it to the chunk's end (each
     // summed in its own direction: a weight near one has an exponent near zero)
     const float c1 = g0 + g1, c2 = c1 + g2, c3 = c2 + g3, r1 = g3 + g2, r0 = r1 + g1;
@@ -694,6 +715,20 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
     if (l == 0) before = 0.f;
     if (l == 15) behind = 0.f;
     total += sum;
+    // the same to the end of the token's sixteen (four lanes)
+    const bool last = (l & 3) == 3;
+    float near = 0.f, sixteen = 0.f;
+    if (!STATES) {
+      float part = r0 + g0;
+#pragma unroll
+      for (int e = 1; e < 4; e <<= 1) {
+        const float w = __shfl_down_sync(0xffffffffu, part, e, 4);
+        if ((l & 3) + e < 4) part += w;
+      }
+      near = __shfl_down_sync(0xffffffffu, part, 1, 4);
+      if (last) near = 0.f;
+      sixteen = __shfl_sync(0xffffffffu, part, 0, 4);
+    }
     if (writes) {
       float2 w01 = make_float2(ex2(r0 + behind) * d4.x, ex2(r1 + behind) * d4.y);
       float2 w23 = make_float2(ex2(g3 + behind) * d4.z, ex2(behind) * d4.w);
@@ -705,10 +740,11 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
         w23 = below_upper(w23);
       }
       if (!STATES) {
-        const float4 cum = make_float4(before + g0, before + c1, before + c2, before + c3);
-        *reinterpret_cast<float4*>(o + SC_CUM) = cum;
-        *reinterpret_cast<float4*>(o + SC_LS) = make_float4(cum.x - __log2f(d4.x), cum.y - __log2f(d4.y),
-                                                            cum.z - __log2f(d4.z), cum.w - __log2f(d4.w));
+        *reinterpret_cast<float4*>(o + SC_CUM) = make_float4(before + g0, before + c1, before + c2, before + c3);
+        const float w0 = r0 + near, w1 = r1 + near, w2 = g3 + near;
+        *reinterpret_cast<float4*>(o + SC_DOWN) = make_float4(w0, w1, w2, last ? sixteen : near);
+        *reinterpret_cast<float4*>(o + SC_COL) =
+            make_float4(w0 + __log2f(d4.x), w1 + __log2f(d4.y), w2 + __log2f(d4.z), near + __log2f(d4.w));
       }
       if (l == 0) reinterpret_cast<float*>(x.sm + K::SM_MISC + MS_TOTAL)[s.st * 2 + h] = ex2(sum);
     }
@@ -841,16 +877,20 @@ __device__ __forceinline__ void role_scores(const Ctx& x) {
     tc_fence_after();
     const float* sc = reinterpret_cast<const float*>(x.sm + K::SM_DEC + s.st * K::SC_SLOT) + sc_off;
     const uint32_t mb = ml + (i & 1) * K::HEADS * K::M_BYTES;
-    const float2 c00 = make_float2(sc[SC_CUM + r0], sc[SC_CUM + r0]), c11 = make_float2(sc[SC_CUM + r0 + 8], sc[SC_CUM + r0 + 8]);
+    // sums from the rows to the end of their sixteen; its total, and those of the sixteens 1 and 2 before it
+    const float down0 = sc[SC_DOWN + r0], down1 = lane < 28 ? sc[SC_DOWN + r0 + 8] : 0.f;
+    const float all = sc[SC_DOWN + 16 * q + 15], mid2 = q == 3 ? sc[SC_DOWN + 47] : 0.f, mid1 = q >= 2 ? sc[SC_DOWN + 31] + mid2 : 0.f;
 #pragma unroll 1
     for (int j = j_first; j <= q >> 1; j += j_step) {  // 32 columns at a time, so that their chains overlap
       float g[16];
       tmem_ld_16x256b_x4_wait(tl + 32 * j, g);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // columns 32 j + 8 k + cl, and the next
-        const float2 ls = *reinterpret_cast<const float2*>(sc + SC_LS + 32 * j + 8 * k + cl);
-        const float2 nls = make_float2(-ls.x, -ls.y);
-        const float2 a0 = __fadd2_rn(c00, nls), a1 = __fadd2_rn(c11, nls);
+        // between the column's sixteen (2 j + k / 2) and the rows' end (the rows' own, or one cut out below: nothing)
+        const float from = 2 * j + (k >> 1) >= q ? 0.f : all + (j > 0 ? 0.f : k < 2 ? mid1 : mid2);
+        const float2 e = *reinterpret_cast<const float2*>(sc + SC_COL + 32 * j + 8 * k + cl);
+        const float2 a0 = __fadd2_rn(make_float2(from - down0, from - down0), e);
+        const float2 a1 = __fadd2_rn(make_float2(from - down1, from - down1), e);
         const float2 m0 = __fmul2_rn(make_float2(g[4 * k], g[4 * k + 1]), make_float2(ex2(a0.x), ex2(a0.y)));
         const float2 m1 = __fmul2_rn(make_float2(g[4 * k + 2], g[4 * k + 3]), make_float2(ex2(a1.x), ex2(a1.y)));
         g[4 * k] = m0.x;
