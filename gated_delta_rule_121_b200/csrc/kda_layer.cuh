@@ -224,7 +224,10 @@ size_t ssm_simt_workspace(int N, int64_t T, int H, int dk, int dv, bool packed);
 cudaError_t launch_ssm_fwd_simt(const SsmArgs& a, void* workspace, bool bf16, cudaStream_t s);
 bool ssm_tc_supported(int dk, int dv, bool bf16);
 size_t ssm_tc_workspace(int N, int64_t T, int H, int G, int dk, int dv, bool packed);
-cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s);
+constexpr uint64_t SSM_WAIT_NS = 2000000000;  // limit of a device-side wait, and the most that can be asked for
+constexpr int SSM_NO_STOP = INT32_MAX;
+cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s, uint64_t wait_ns = SSM_WAIT_NS,
+                              int stop_at = SSM_NO_STOP);
 cudaError_t launch_ssm_step(const SsmArgs& a, float* state, bool bf16, cudaStream_t s);
 
 // True when every row of `p` starts on a boundary of `bytes` (a power of two).

@@ -3,7 +3,7 @@
 // allocates or synchronises.
 #include <cstdint>
 
-#include "../../include/kda.h"
+#include "../../include/kda_testing.h"
 #include "kda_layer.cuh"
 
 namespace {
@@ -44,6 +44,41 @@ kda_status_t check_ssm(const void* x, int64_t ldx, const void* b, int64_t ldb, c
   for (const void* p : {x, b, c, (const void*)A_log, (const void*)D, (const void*)dt_bias, out})
     if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
   return KDA_OK;
+}
+
+kda_status_t ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
+                     const float* delta, const float* A_log, const float* D, const float* dt_bias,
+                     const float* init_state, void* out, float* final_state, int B, int64_t T, int H, int G,
+                     int dk, int dv, const int32_t* cu_seqlens, void* stream, kda_dtype_t dt, void* workspace,
+                     size_t workspace_bytes, uint64_t wait_ns = kda::SSM_WAIT_NS, int stop_at = kda::SSM_NO_STOP) {
+  if (B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
+  if (T > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  const int64_t tokens = cu_seqlens ? T : (int64_t)B * T;
+  if (tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  const kda_status_t st =
+      check_ssm(x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, out, H, G, dk, dv, dt, tokens == 0 || B == 0);
+  if (st != KDA_OK) return st;
+  for (const void* p : {(const void*)init_state, (const void*)final_state, (const void*)cu_seqlens})
+    if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+  if ((int64_t)B * H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < kda_ssm_fwd_workspace_size(B, T, H, G, dk, dv, cu_seqlens != nullptr, dt))
+    return KDA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  kda::DeviceStatus* status = reinterpret_cast<kda::DeviceStatus*>(workspace);
+  if (cudaMemsetAsync(status, 0, sizeof(kda::DeviceStatus), s) != cudaSuccess) return KDA_ERR_CUDA;
+  if (B == 0) return KDA_OK;
+  const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state,
+                       B, T, H, G, dk, dv, cu_seqlens, status};
+  if (tokens == 0) {  // nothing to walk: the states alone
+    if (!final_state) return KDA_OK;
+    const size_t bytes = (size_t)B * H * dk * dv * sizeof(float);
+    if (!init_state) return result(cudaMemsetAsync(final_state, 0, bytes, s));
+    if (final_state == init_state) return KDA_OK;
+    return result(cudaMemcpyAsync(final_state, init_state, bytes, cudaMemcpyDeviceToDevice, s));
+  }
+  if (kda::ssm_tc_supported(dk, dv, dt == KDA_BF16)) return result(kda::launch_ssm_fwd_tc(a, workspace, s, wait_ns, stop_at));
+  return result(kda::launch_ssm_fwd_simt(a, workspace, dt == KDA_BF16, s));
 }
 
 }  // namespace
@@ -88,34 +123,19 @@ kda_status_t kda_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb,
                          const float* init_state, void* out, float* final_state, int B, int64_t T, int H, int G,
                          int dk, int dv, const int32_t* cu_seqlens, void* stream, kda_dtype_t dt, void* workspace,
                          size_t workspace_bytes) {
-  if (B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
-  if (T > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
-  const int64_t tokens = cu_seqlens ? T : (int64_t)B * T;
-  if (tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
-  const kda_status_t st =
-      check_ssm(x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, out, H, G, dk, dv, dt, tokens == 0 || B == 0);
-  if (st != KDA_OK) return st;
-  for (const void* p : {(const void*)init_state, (const void*)final_state, (const void*)cu_seqlens})
-    if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
-  if ((int64_t)B * H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < kda_ssm_fwd_workspace_size(B, T, H, G, dk, dv, cu_seqlens != nullptr, dt))
-    return KDA_ERR_WORKSPACE;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  kda::DeviceStatus* status = reinterpret_cast<kda::DeviceStatus*>(workspace);
-  if (cudaMemsetAsync(status, 0, sizeof(kda::DeviceStatus), s) != cudaSuccess) return KDA_ERR_CUDA;
-  if (B == 0) return KDA_OK;
-  const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state,
-                       B, T, H, G, dk, dv, cu_seqlens, status};
-  if (tokens == 0) {  // nothing to walk: the states alone
-    if (!final_state) return KDA_OK;
-    const size_t bytes = (size_t)B * H * dk * dv * sizeof(float);
-    if (!init_state) return result(cudaMemsetAsync(final_state, 0, bytes, s));
-    if (final_state == init_state) return KDA_OK;
-    return result(cudaMemcpyAsync(final_state, init_state, bytes, cudaMemcpyDeviceToDevice, s));
-  }
-  if (kda::ssm_tc_supported(dk, dv, dt == KDA_BF16)) return result(kda::launch_ssm_fwd_tc(a, workspace, s));
-  return result(kda::launch_ssm_fwd_simt(a, workspace, dt == KDA_BF16, s));
+  return ssm_fwd(x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state, B, T, H, G, dk, dv,
+                 cu_seqlens, stream, dt, workspace, workspace_bytes);
+}
+
+// (test hook, include/kda_testing.h)
+kda_status_t kda_testing_ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
+                                 const float* delta, const float* A_log, const float* D, const float* dt_bias,
+                                 const float* init_state, void* out, float* final_state, int B, int64_t T, int H,
+                                 int G, int dk, int dv, const int32_t* cu_seqlens, void* stream, kda_dtype_t dt,
+                                 void* workspace, size_t workspace_bytes, uint64_t wait_ns, int stop_at) {
+  if (!kda::ssm_tc_supported(dk, dv, dt == KDA_BF16)) return KDA_ERR_UNSUPPORTED;
+  return ssm_fwd(x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, init_state, out, final_state, B, T, H, G, dk, dv,
+                 cu_seqlens, stream, dt, workspace, workspace_bytes, wait_ns, stop_at);
 }
 
 kda_status_t kda_ssm_step(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,

@@ -154,6 +154,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint
       "l"(tmap), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int c0, int c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1) : "memory");
 }
@@ -299,6 +304,8 @@ struct TcArgs {
   int hpt, tiles;  // heads per tile, tiles of 128 columns
   int items;       // pieces times tiles
   int blocks, per_block;  // of the second pass, and items of a block there
+  uint32_t wait_ns;       // limit of the waits
+  int stop_at;            // a test's: the loads' role stands still before this chunk
 };
 
 // ------------------------------------------------------------------ roles
@@ -346,16 +353,19 @@ struct Walk {
   }
 };
 
-// Bounded wait that also gives up once another role has: the first to give up
-// raises the block's flag (looked at every 256 tests), and from then on no wait of
-// the block waits long.  The roles that only compute run on over whatever is
-// there (every access stays inside its buffers) and do not look at the result;
-// the ones that start copies or products stop.  All that is waited for are the
-// block's own loads and products.  Written as one block, so that a wait that
-// finds its phase complete takes three instructions (and without a time hint:
-// with one, a wait becomes a loop of sleeps that takes issue slots from the other
-// roles and wakes late).
-constexpr uint32_t MAX_TESTS = 1u << 23;  // some tenths of a second: a test takes about 50 ns
+// A role's wait.  It ends once the block's abort flag is raised, which it looks at
+// every 256 tests.  The loads' role raises it (wait_warp): where anything of a block
+// stands still, so does that role, which lives as long as the block has work, and
+// it measures the time.  Behind that stands a limit of tests, for the
+// case that the loads' role itself is not there any more.  The roles that only
+// compute run on over whatever is there (every access stays inside its
+// buffers) and do not look at the result; the ones that start copies or
+// products stop.  All that is waited for are the block's own loads and products.
+// Written as one block, so that a wait that finds its phase complete takes three
+// instructions (and without a time hint: with one, a wait becomes a loop of sleeps
+// that takes issue slots from the other roles and wakes late; with a clock in
+// every wait a 64K prompt takes 2 % longer).
+constexpr uint32_t MAX_TESTS = 1u << 27;  // of the phase's barrier: a test takes some 50 ns
 __device__ __forceinline__ bool wait_at(uint32_t bars, uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -391,19 +401,39 @@ __device__ __forceinline__ void commit(const Ctx& x, int bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(x.bars + 8 * bar)
                : "memory");
 }
-// A copy or product in flight has ended, whatever else the block gave up.
-__device__ __forceinline__ void land(uint32_t bar, uint32_t parity) {
+// The loads' role's waits, by wall time, and for all lanes of its warp alike.
+__device__ __forceinline__ bool test_256(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
       "mov.u32 n, 0;\n"
       "TEST:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE;\n\t"
       "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, %2;\n\t"
+      "setp.lt.u32 q, n, 256;\n\t"
       "@q bra TEST;\n"
-      "DONE:\n\t}" ::"r"(bar), "r"(parity), "n"(MAX_TESTS)
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
       : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_warp(const Ctx& x, int bar, uint32_t parity, uint32_t ns) {
+  const uint32_t at = x.bars + 8 * bar;
+  if (__all_sync(0xffffffffu, test_256(at, parity))) return true;
+  const uint32_t t0 = globaltimer_lo();  // (turns over after 4.3 s: twice the longest limit)
+  do {
+    if (__all_sync(0xffffffffu, test_256(at, parity))) return true;
+  } while (__all_sync(0xffffffffu, globaltimer_lo() - t0 < ns));
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(x.bars + MS_ABORT), "r"(1) : "memory");
+  return false;
+}
+// A copy or product in flight has ended, whatever else the block gave up.
+__device__ __forceinline__ void land(uint32_t bar, uint32_t parity) {
+  const uint32_t t0 = globaltimer_lo();
+  while (!test_256(bar, parity) && globaltimer_lo() - t0 < SSM_WAIT_NS) {}
 }
 // A chunk's stage in a ring of N and the parity of its use, counted along.
 template <int N>
@@ -462,19 +492,19 @@ __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const v
   };
 #pragma unroll 1
   for (int i = -K::NX; i < x.nchunks; ++i) {  // chunk i's store; the loads run ahead
+    if (i == t.stop_at && !wait_warp(x, B_DRAIN, 0, t.wait_ns)) break;
     if (leader && i >= 0 && wx.tok + 2 * CH < wx.end) {  // into L2, a chunk before its load
       for (int e = 0; e < atoms; ++e) tma_prefetch_2d(tx, wx.h0 * DV + 64 * e, wx.tok + 2 * CH);
     }
     // k, s: the stages of chunks i + NB, i + NX, which are those of chunk i
     if (i + K::NB >= 0 && i + K::NB < x.nchunks) {
-      if (i >= 0 && !wait_bar(x, B_KFREE + k.st, k.ph ^ 1)) break;
+      if (i >= 0 && !wait_warp(x, B_KFREE + k.st, k.ph ^ 1, t.wait_ns)) break;
       load_k();
     }
     if (!STATES && i >= 0) {
       wo.next(x);
       const int st = i % K::NX;
-      if (!wait_bar(x, B_YOUT + st, (i / K::NX) & 1)) break;
-      __syncwarp();
+      if (!wait_warp(x, B_YOUT + st, (i / K::NX) & 1, t.wait_ns)) break;
       const int v = min(wo.end - wo.tok, CH), col = wo.h0 * DV;
       const uint32_t at = K::SM_X + st * K::X_BYTES;
       if (v == CH) {
@@ -496,11 +526,13 @@ __device__ __forceinline__ void role_move(const Ctx& x, const TcArgs& t, const v
       }
     }
     if (i + K::NX < x.nchunks) {
-      if (STATES && i >= 0 && !wait_bar(x, B_XFREE + s.st, s.ph ^ 1)) break;
+      if (STATES && i >= 0 && !wait_warp(x, B_XFREE + s.st, s.ph ^ 1, t.wait_ns)) break;
       __syncwarp();
       load_x();
     }
   }
+  // The last chunk has been used (a chunk's y has: the loop above has waited for it).
+  if (STATES && nx > 0 && nx == x.nchunks) wait_warp(x, B_XFREE + (nx - 1) % K::NX, ((nx - 1) / K::NX) & 1, t.wait_ns);
   // No copy stays in flight behind the block: the latest load of every stage, and every store.
 #pragma unroll 1
   for (int i = 0; i < MAXST; ++i) {
@@ -1258,10 +1290,12 @@ size_t ssm_tc_workspace(int N, int64_t T, int H, int G, int dk, int dv, bool pac
   return plan(N, T, H, G, dk, dv, packed).total;
 }
 
-cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_ssm_fwd_tc(const SsmArgs& a, void* workspace, cudaStream_t s, uint64_t wait_ns, int stop_at) {
   const PiecePlan p = plan(a.N, a.T, a.H, a.G, a.dk, a.dv, a.cu != nullptr);
   TcArgs t;
   t.a = a;
+  t.wait_ns = (uint32_t)std::min<uint64_t>(wait_ns, SSM_WAIT_NS);
+  t.stop_at = stop_at;
   t.hpt = heads_per_tile(a.H, a.G, a.dv);
   t.tiles = a.H / t.hpt;
   t.items = (int)(p.pieces * t.tiles);

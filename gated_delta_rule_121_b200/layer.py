@@ -214,7 +214,8 @@ def kda_ssm_fwd(x, b, c, delta, A_log, D=None, dt_bias=None, init_state=None, cu
     """Selective state-space scan over whole sequences (include/kda.h,
     kda_ssm_fwd).  x [B,T,H,dv], b and c [B,T,G,dk] (tokens any distance apart),
     delta [B,T,H], A_log, D and dt_bias [H] fp32, states [N,H,dk,dv] fp32.
-    Returns ``(out, final_state)``."""
+    Returns ``(out, final_state)``.  With a ``workspace`` of one's own,
+    kda_workspace_status tells afterwards whether a device-side wait gave up."""
     if x.dim() != 4 or b.dim() != 4 or c.dim() != 4:
         raise ValueError("x must be [B, T, H, dv], b and c [B, T, G, dk]")
     dt, dev, H, G, dk, dv, head = _ssm_args(x, b, c, delta, A_log, D, dt_bias, 2)

@@ -55,6 +55,26 @@ KDA_API kda_status_t kda_testing_fwd(const void *q, const void *k, const void *v
                              void *workspace, size_t workspace_bytes,
                              float *debug_out, uint64_t wait_ns, int inject_stuck);
 
+/*
+ * Same as kda_ssm_fwd on the tensor-core path (else KDA_ERR_UNSUPPORTED), plus
+ *   wait_ns    bound for a block that stands still, in nanoseconds (kda_ssm_fwd
+ *              uses 2e9, the most that counts here).
+ *   stop_at    the warp of each block that loads its inputs waits before chunk
+ *              stop_at of the block (64 tokens each; negative: during the loads
+ *              that run ahead of the first chunk; INT32_MAX: never) until the
+ *              block's products have all ended, which they cannot without the
+ *              loads that are left.  It gives up after wait_ns and the other
+ *              warps with it, KDA_ERR_TIMEOUT is recorded in the workspace status
+ *              word, and the block unwinds as kda_fwd's do: copies and tensor-core
+ *              work drained, tensor memory released.
+ */
+KDA_API kda_status_t kda_testing_ssm_fwd(const void *x, int64_t ldx, const void *b, int64_t ldb, const void *c,
+                             int64_t ldc, const float *delta, const float *A_log, const float *D,
+                             const float *dt_bias, const float *init_state, void *out, float *final_state,
+                             int B, int64_t T, int H, int G, int dk, int dv, const int32_t *cu_seqlens,
+                             void *stream, kda_dtype_t dt, void *workspace, size_t workspace_bytes,
+                             uint64_t wait_ns, int stop_at);
+
 /* 1 when kda_fwd uses the tensor-core kernel for this shape, else 0. */
 KDA_API int kda_testing_fwd_path(int dk, int dv, kda_dtype_t dt);
 
