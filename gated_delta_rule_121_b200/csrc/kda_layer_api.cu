@@ -18,6 +18,18 @@ bool dtype_ok(kda_dtype_t dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 int esize(kda_dtype_t dt) { return dt == KDA_BF16 ? 2 : 4; }
 kda_status_t result(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
+// Whether the dense `out` of `rows` rows of `width` elements shares memory with `rows`
+// rows of `in_width` elements, `ld` apart.  (Between the rows of a slice it may lie.)
+bool shares(const void* out, int64_t width, const void* in, int64_t in_width, int64_t ld, int64_t rows, kda_dtype_t dt) {
+  if (!out || !in || rows <= 0) return false;
+  const __int128 start = (__int128)reinterpret_cast<uintptr_t>(out) - (__int128)reinterpret_cast<uintptr_t>(in);
+  const __int128 end = start + (__int128)rows * width * esize(dt);
+  const __int128 step = (__int128)ld * esize(dt), row = (__int128)in_width * esize(dt);
+  if (start >= (rows - 1) * step + row) return false;  // behind the last row
+  const __int128 first = start < row ? 0 : (start - row) / step + 1;  // the first row that ends behind `start`
+  return first * step < end;
+}
+
 kda_status_t check_conv(const void* x, int64_t ldx, const float* weight, const float* bias, const void* out, int C,
                         int K, kda_act_t act, kda_dtype_t dt, bool empty) {
   if (C <= 0 || ldx < C || !dtype_ok(dt)) return KDA_ERR_INVALID_ARG;
@@ -46,6 +58,14 @@ kda_status_t check_ssm(const void* x, int64_t ldx, const void* b, int64_t ldb, c
   return KDA_OK;
 }
 
+// The same of the scan's token inputs: heads and tokens are done in any order.
+bool shares_any(const void* out, const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc, int H,
+                int G, int dk, int dv, int64_t rows, kda_dtype_t dt) {
+  const int64_t width = (int64_t)H * dv, keys = (int64_t)G * dk;
+  return shares(out, width, x, width, ldx, rows, dt) || shares(out, width, b, keys, ldb, rows, dt) ||
+         shares(out, width, c, keys, ldc, rows, dt);
+}
+
 kda_status_t ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, const void* c, int64_t ldc,
                      const float* delta, const float* A_log, const float* D, const float* dt_bias,
                      const float* init_state, void* out, float* final_state, int B, int64_t T, int H, int G,
@@ -64,6 +84,7 @@ kda_status_t ssm_fwd(const void* x, int64_t ldx, const void* b, int64_t ldb, con
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < kda_ssm_fwd_workspace_size(B, T, H, G, dk, dv, cu_seqlens != nullptr, dt))
     return KDA_ERR_WORKSPACE;
+  if (B > 0 && shares_any(out, x, ldx, b, ldb, c, ldc, H, G, dk, dv, tokens, dt)) return KDA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   kda::DeviceStatus* status = reinterpret_cast<kda::DeviceStatus*>(workspace);
   if (cudaMemsetAsync(status, 0, sizeof(kda::DeviceStatus), s) != cudaSuccess) return KDA_ERR_CUDA;
@@ -95,7 +116,7 @@ kda_status_t kda_conv_fwd(const void* x, int64_t ldx, const float* weight, const
   if (st != KDA_OK) return st;
   for (const void* p : {init_state, (const void*)final_state, (const void*)cu_seqlens})
     if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
-  if (out == x && tokens > 0) return KDA_ERR_INVALID_ARG;  // a token reads the ones before it
+  if (shares(out, C, x, C, ldx, tokens, dt)) return KDA_ERR_INVALID_ARG;  // a token reads the ones before it
   if (B == 0) return KDA_OK;
   const kda::ConvArgs a{x, ldx, weight, bias, init_state, out, final_state, B, T, C, K, cu_seqlens, act};
   return result(kda::launch_conv_fwd(a, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
@@ -107,6 +128,7 @@ kda_status_t kda_conv_step(const void* x, int64_t ldx, const float* weight, cons
   const kda_status_t st = check_conv(x, ldx, weight, bias, out, C, K, act, dt, B == 0);
   if (st != KDA_OK) return st;
   if ((B > 0 && !state) || !aligned16(state)) return KDA_ERR_INVALID_ARG;
+  if (shares(out, C, x, C, ldx, B, dt)) return KDA_ERR_INVALID_ARG;  // sequences in any order
   if (B == 0) return KDA_OK;
   const kda::ConvArgs a{x, ldx, weight, bias, nullptr, out, state, B, 1, C, K, nullptr, act};
   return result(kda::launch_conv_step(a, dt == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
@@ -147,6 +169,7 @@ kda_status_t kda_ssm_step(const void* x, int64_t ldx, const void* b, int64_t ldb
   if (st != KDA_OK) return st;
   if ((B > 0 && !state) || !aligned16(state)) return KDA_ERR_INVALID_ARG;
   if ((int64_t)B * H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (shares_any(out, x, ldx, b, ldb, c, ldc, H, G, dk, dv, B, dt)) return KDA_ERR_INVALID_ARG;
   if (B == 0) return KDA_OK;
   const kda::SsmArgs a{x, ldx, b, ldb, c, ldc, delta, A_log, D, dt_bias, nullptr, out, nullptr,
                        B, 1, H, G, dk, dv, nullptr, nullptr};
@@ -168,6 +191,8 @@ kda_status_t kda_group_norm(const void* x, int64_t ldx, const void* gate, int64_
   // An output that is also an input is dense, so that every thread writes where it has read.
   if (rows > 1 && ((out == x && ldx != C) || (out == gate && gate && ldg != C))) return KDA_ERR_INVALID_ARG;
   if (width > kda::NORM_MAX_WIDTH || rows > (int64_t)INT32_MAX / groups) return KDA_ERR_UNSUPPORTED;
+  if ((out != x && shares(out, C, x, C, ldx, rows, dt)) || (out != gate && shares(out, C, gate, C, ldg, rows, dt)))
+    return KDA_ERR_INVALID_ARG;
   if (rows == 0) return KDA_OK;
   const kda::NormArgs a{x, ldx, gate, ldg, weight, bias, out, rows, groups, width, shared ? 1 : 0,
                         eps, center ? 1 : 0, act, gate_first ? 1 : 0};

@@ -4,7 +4,8 @@ prompts and for single tokens.
 
 Argument marshalling only.  Token tensors may be slices of a wider one (a fused
 projection, a convolution's output): the last dimensions are dense, tokens lie
-any distance apart.  A tensor that an entry point cannot read as it lies raises
+any distance apart.  ``out`` shares no memory with them (kda_group_norm's may be x
+or gate).  A tensor that an entry point cannot read as it lies raises
 ValueError; nothing is copied behind the caller's back.
 
 Each call runs on the tensors' device, on ``stream`` (its current stream by
@@ -131,7 +132,7 @@ def kda_conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None, activat
     kda_conv_fwd).  x [B,T,C] (tokens any distance apart), weight [C,K] and bias
     [C] fp32, init_state [N,K-1,C] in x's type.  Returns ``(out, final_state)``;
     final_state [N,K-1,C] holds the last K-1 inputs of each sequence and may be
-    init_state itself.  ``out`` must not overlap x."""
+    init_state itself."""
     dt, dtype, dev = _dtype(x), x.dtype, x.get_device()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, C]")

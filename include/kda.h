@@ -454,7 +454,9 @@ KDA_API kda_status_t kda_decode_spec_gated(const void *q_prev, const void *k_pre
  * row's own width.  Outputs, states and parameters are dense.  Parameters
  * (weights, biases, A_log, D, dt_bias), delta and recurrent states are fp32.
  * The convolution's x, the norm's x and gate, and delta may start at any element;
- * every other pointer is 16-byte aligned as above.
+ * every other pointer is 16-byte aligned as above.  An `out` that shares memory
+ * with rows of x, b, c or gate is refused (KDA_ERR_INVALID_ARG), but for the norm's
+ * in-place form; between the rows of a slice it may lie.
  * --------------------------------------------------------------------- */
 typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 } kda_act_t;
 
