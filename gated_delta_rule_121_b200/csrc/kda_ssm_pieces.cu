@@ -2,10 +2,17 @@
 // table of a packed batch, whose lengths are on the device.
 #include "kda_ssm_pieces.cuh"
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
-constexpr int MAX_PARTS = 64;  // of a sequence of known length
+constexpr int MAX_PARTS = 64;   // of a sequence of known length
+// And of all sequences of a batch, in numbers of blocks that the device holds at a
+// time: it bounds the workspace (155 MB for the largest states) for any length, so
+// that the bound grows with the length.  By the cost model below no batch loses more
+// than 2.5 % by it, and only some of more than 24K tokens a sequence do.
+constexpr int MAX_WAVES = 16;
 
 // The pieces of a packed batch (one block): first the ones that others follow,
 // which are whole, then the last ones by length, the longest first, so that blocks
@@ -116,18 +123,20 @@ __global__ void __launch_bounds__(CT) ssm_compose_kernel(PieceArgs p, bool init,
 PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, int least, int H, int dk, int dv,
                       bool packed) {
   PiecePlan p;
+  int64_t room;  // slots and pieces beyond the sequences that any shorter or smaller batch may need
   const int64_t chunks = (T + PIECE_CHUNK - 1) / PIECE_CHUNK;  // of a sequence, or of the packed total
   if (!packed) {
     // Pieces per sequence and parts per piece with the fewest chunk times in the
     // two passes, in waves of blocks; 3 chunk times for a block's start and 6 for
     // the second launch.
-    const int64_t chains = (int64_t)N * blocks;
+    const int64_t chains = (int64_t)N * blocks, shortest = chunks / least;
+    room = shortest < 2 ? 0 : std::min(N * std::min<int64_t>(MAX_PARTS, shortest), (int64_t)MAX_WAVES * places / blocks);
     auto waves = [&](int64_t n) { return (double)((n + places - 1) / places); };
     int64_t part = chunks > 0 ? chunks : 1;
     int parts = 1;
     double cost = waves(chains) * chunks;
     for (int r = 2; r <= MAX_PARTS; ++r)
-      for (int q = 1; q <= 4 && r * q <= MAX_PARTS && chunks / (r * q) >= least; ++q) {
+      for (int q = 1; q <= 4 && r * q <= MAX_PARTS && chunks / (r * q) >= least && (int64_t)N * r * q <= room; ++q) {
         const int64_t len = (chunks + r * q - 1) / (r * q);
         const double c = waves(chains * r) * (len * q + 3) + first * waves(chains * (r - 1) * q) * (len + 3) + 6;
         if (c < cost) {
@@ -155,15 +164,16 @@ PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, in
     p.first_pass = T > p.len ? T / p.len : 0;  // the pieces that others follow are whole
     // a sequence of L > len tokens has at most L / len + 1 < 2 L / len pieces
     p.slots = p.first_pass ? 2 * T / p.len : 0;
+    room = std::min<int64_t>(2 * T / (least * PIECE_CHUNK), 4 * (int64_t)places / blocks);
   }
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   size_t off = 256;  // the status word
   p.table = off;
-  if (packed) off += up((size_t)p.pieces * sizeof(PieceEntry));
+  if (packed) off += up((size_t)(N + room / 2 + 1) * sizeof(PieceEntry));
   p.decay = off;
-  off += up((size_t)p.slots * H * sizeof(float));
+  off += up((size_t)room * H * sizeof(float));
   p.state = off;
-  off += (size_t)p.slots * H * dk * dv * sizeof(float);
+  off += (size_t)room * H * dk * dv * sizeof(float);
   p.total = off;
   return p;
 }

@@ -62,7 +62,7 @@ struct PiecePlan {
   int per_seq, parts;
   int64_t len, part, slots;           // tokens per piece and part; slots and the blocks: upper bounds for packed batches
   int64_t pieces, first_pass;         // pieces in all, and parts of the first pass (0: there is none)
-  size_t table, decay, state, total;  // workspace offsets, the status word first
+  size_t table, decay, state, total;  // workspace offsets, the status word first; they grow with N and T
 };
 // `blocks` blocks per piece; `places` blocks at a time on the device; `first` the
 // cost of a chunk of the first pass against one of the second; parts of at

@@ -511,7 +511,9 @@ KDA_API kda_status_t kda_conv_step(const void *x, int64_t ldx, const float *weig
  *   dk, dv in {16, 32, 64, 128}.  ldx, ldb, ldc times the element size must
  *   be multiples of 16 bytes (KDA_ERR_INVALID_ARG).
  *   workspace  at least kda_ssm_fwd_workspace_size(...) bytes (packed: nonzero
- *              with cu_seqlens, T then the total token count and B = N).  Its
+ *              with cu_seqlens, T then the total token count and B = N).  The size
+ *              never falls as B or T grow: one made for the largest batch and the
+ *              longest prompt serves all others of those heads.  Its
  *              contents on entry do not matter; kda_workspace_status reads
  *              its status word.
  * fp32 inputs, and sizes other than dk, dv in {64, 128}, run in fp32 on CUDA
