@@ -146,6 +146,13 @@ __device__ __forceinline__ float log1p_unit(float e) {
 // softplus(d) = log(1 + e^d) without overflow: max(d, 0) + log(1 + e^-|d|).
 __device__ __forceinline__ float softplus_f32(float d) { return fmaxf(d, 0.f) + log1p_unit(expf(-fabsf(d))); }
 
+// exp(A_log), kept where its product with log2(e) is finite: with an infinite rate a step
+// of zero, which leaves the state as it is, would make it no number.  Not a number stays so.
+__device__ __forceinline__ float decay_rate(float A_log) {
+  const float r = expf(A_log);
+  return r > 2e38f ? 2e38f : r;
+}
+
 // Sequences of a token tensor: N of T tokens each, or packed by offsets.
 // Offsets are cut off at the tensor's T tokens, so that bad ones never lead
 // outside it.

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(ScanShape<DK, DV>::NT)
   const IO* b = (const IO*)a.b + (int64_t)grp * DK;
   const IO* c = (const IO*)a.c + (int64_t)grp * DK;
   IO* out = (IO*)a.out + (int64_t)h * DV + col0 + p;
-  const float rate = -expf(a.A_log[h]) * 1.4426950408889634f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float rate = -decay_rate(a.A_log[h]) * 1.4426950408889634f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const float skip = a.D ? a.D[h] : 0.f;
 
   // Row j of piece k of this thread: 4 (rg + RG k) + j.
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(StepShape<DK, DV>::NT)
   }
   float d = a.delta[bh];
   if (a.dt_bias) d = softplus_f32(d + a.dt_bias[h]);
-  const float av = expf(-expf(a.A_log[h]) * d), skip = a.D ? a.D[h] : 0.f;
+  const float av = expf(-decay_rate(a.A_log[h]) * d), skip = a.D ? a.D[h] : 0.f;
   const float4 x = make_float4(to_f32(xp[0]), to_f32(xp[1]), to_f32(xp[2]), to_f32(xp[3]));
   const float4 dx = make_float4(d * x.x, d * x.y, d * x.z, d * x.w);
   __syncthreads();

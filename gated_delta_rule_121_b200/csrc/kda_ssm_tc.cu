@@ -709,7 +709,7 @@ __device__ __forceinline__ void role_decay(const Ctx& x, const TcArgs& t, int wh
     if (m < 0) continue;
     const int i = m * K::DECS + which;
     if (wp.next(x) || m == 0) {  // a new item
-      rate = -expf(a.A_log[wp.h0 + h]) * LOG2E;
+      rate = -decay_rate(a.A_log[wp.h0 + h]) * LOG2E;
       bias = soft ? a.dt_bias[wp.h0 + (lane & sh)] : 0.f;
     }
     const int v = min(wp.end - wp.tok, CH);

@@ -7,7 +7,9 @@ import math
 import pytest
 import torch
 
+import gated_delta_rule_121_b200 as kda
 from layer_inputs import offsets, randn, scan_inputs
+from oracle import layer as ref
 from test_gpu_layer_scan import compare, run
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +80,23 @@ def test_steps_of_float32s_range(dk, dv):
         d[k][:, 20] *= 1e-5  # the state after it: of order 1e23
     out, fin = run(d, randn(g, 1, 2, dk, dv), None)
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(fin).all())
+
+
+@pytest.mark.parametrize("dtype,dk,dv", SIZES)
+@pytest.mark.parametrize("A_log", [88.0, 89.5, 300.0])
+def test_rates_beyond_float32(dtype, dk, dv, A_log):
+    """exp(A_log) beyond fp32's range: a step of zero leaves the state, any other resets it."""
+    d, g = scan_inputs(106, (1, 90), 2, 1, dk, dv, dtype)
+    d["A_log"].fill_(A_log)
+    d["delta"][:, 30:50] = -700.0
+    init = randn(g, 1, 2, dk, dv)
+    r = compare(*run(d, init, None), d, init, None)
+    state = init.clone()
+    for t in (0, 30, 31):  # a reset and two steps of zero, token by token
+        a = [d[k][:, t].contiguous() for k in ("x", "b", "c", "delta")]
+        out = kda.kda_ssm_step(*a, d["A_log"], state, d["D"], d["dt_bias"])
+        assert bool(torch.isfinite(out).all())
+        if t == 0:
+            after = state.clone()
+            ref.assert_within(out, r["out"][:, 0], r["err_out"][:, 0], "step")
+    assert torch.equal(state, after)
