@@ -518,8 +518,11 @@ KDA_API kda_status_t kda_conv_step(const void *x, int64_t ldx, const float *weig
  *              its status word.
  * fp32 inputs, and sizes other than dk, dv in {64, 128}, run in fp32 on CUDA
  * cores; bf16 with dk, dv in {64, 128} runs on the tensor cores with bf16
- * operands and fp32 accumulation (any bf16 magnitude; the state itself is
- * fp32 and the operands that update it carry 24 bits).  A non-finite input
+ * operands and fp32 accumulation.  The state is fp32, and the operands that
+ * update it carry 24 bits (where |D_t x_t| lies between 2^-100 and bf16's largest
+ * value; fewer below).  Scores and state enter an output rounded to bf16, so that it
+ * is off by 2^-8 of the sum of its terms' magnitudes, which shows where they cancel.
+ * Decays may be of any size in all forms.  A non-finite input
  * spoils the outputs of its own sequence only: from its 64-token chunk on.
  */
 KDA_API size_t kda_ssm_fwd_workspace_size(int B, int64_t T, int H, int G, int dk, int dv, int packed,
@@ -556,7 +559,8 @@ KDA_API kda_status_t kda_ssm_step(const void *x, int64_t ldx, const void *b, int
  *           by all groups when `shared` is nonzero
  *   out     [rows, groups*width] dtype dt, dense; may be x or gate itself when
  *           that one is dense (each element is read before it is written)
- * Statistics are two-pass (mean, then centred squares) in fp32.  width <= 16384.
+ * Statistics are two-pass (mean, then centred squares) in fp32: magnitudes of u
+ * up to 1e17, whose squares' sum fp32 holds.  width <= 16384.
  * No workspace.
  */
 KDA_API kda_status_t kda_group_norm(const void *x, int64_t ldx, const void *gate, int64_t ldg,
