@@ -9,10 +9,14 @@
 // loads go out before the first product, the K - 1 inputs before them stay in
 // registers, and the weights are loaded once for all its runs.  A block spans up
 // to 256 threads' channels of the same tokens, whole DRAM pages of a row.  A run
-// that a sequence's border cuts is done token by token.
-// Measured: 64K tokens of 12288 bf16 channels 576 us, 5.6 TB/s, 85 % of a copy's
-// rate; the rest is latency between a thread's batches (requesting the next
-// batch's rows one by one as this one's are used was slower, 790 us).
+// that a sequence's border cuts is done token by token, and so is a thread's run
+// behind one that ended with its sequence (64K tokens of 1112 channels: 82 us as one
+// sequence, 89 in sequences of 64, 247 in sequences of 16).
+// Measured: 64K tokens of 12288 bf16 channels 577 us, 5.6 TB/s, 85 % of a copy's
+// rate, and 606 us as a slice of rows three times as wide; the rest is latency
+// between a thread's batches (requesting the next batch's rows one by one as this
+// one's are used was slower, 790 us).  Channels that 4 does not divide are taken
+// one by one: 1110 of them 100 us, 44 % of a copy's rate, where 1112 take 82.
 #include "kda_layer.cuh"
 
 namespace kda {

@@ -9,7 +9,9 @@
 // bandwidth bounds it: 6 bytes per bf16 element with a gate, 4 without.
 // Measured: 64K rows of 96 groups of 128, bf16 with a gate, 0.71 to 0.81 ms (by where
 // the buffers lie), 6.0 to 6.8 TB/s, a copy's rate; 512 rows of one group of 6144 8
-// us, most of it the launch.
+// us, most of it the launch.  Groups or rows off 16-byte boundaries are taken element
+// by element, which is bound by the accesses: 16K rows of 96 groups of 128 take 188 us,
+// of 100 465.
 #include "kda_layer.cuh"
 
 namespace kda {

@@ -128,7 +128,11 @@ PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, in
   if (!packed) {
     // Pieces per sequence and parts per piece with the fewest chunk times in the
     // two passes, in waves of blocks; 3 chunk times for a block's start and 6 for
-    // the second launch.
+    // what comes between the passes.  (Tensor cores, in the second pass's chunks of 2
+    // us: a block's start is 6 to 7 us, the composition 4 to 12 for 4 to 32 parts, a chunk
+    // of the first pass 0.95.  CUDA cores, fp32, 64 x 32: a chunk takes 14 us, one of the
+    // first pass 8; starts and composition are the smaller there, and cuts a little
+    // coarser than they could be.)
     const int64_t chains = (int64_t)N * blocks, shortest = chunks / least;
     room = shortest < 2 ? 0 : std::min(N * std::min<int64_t>(MAX_PARTS, shortest), (int64_t)MAX_WAVES * places / blocks);
     auto waves = [&](int64_t n) { return (double)((n + places - 1) / places); };

@@ -70,10 +70,11 @@ struct PiecePlan {
 PiecePlan plan_pieces(int N, int64_t T, int blocks, int places, double first, int least, int H, int dk, int dv, bool packed);
 // The pieces' part of a launch's arguments, and for packed batches their table.
 cudaError_t prepare_pieces(const PiecePlan& p, const SsmArgs& a, void* workspace, PieceArgs* out, cudaStream_t s);
-// The launches from the first pass on overlap: a kernel lets the next one's blocks
-// start as soon as all of its own have (start_next), and that one waits for the
-// kernel before it to end, with all its writes, before it touches what they share
-// (await_last).  A launch, a block's barriers and TMEM are ready by then.
+// On the tensor-core path the launches from the first pass on overlap: a kernel lets
+// the next one's blocks start as soon as all of its own have (start_next), and that one
+// waits for the kernel before it to end, with all its writes, before it touches what
+// they share (await_last).  A launch, a block's barriers and TMEM are ready by then.
+// (The CUDA-core path's passes neither let a kernel start early nor start early.)
 __device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>

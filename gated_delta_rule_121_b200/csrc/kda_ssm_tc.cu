@@ -35,7 +35,8 @@
 // carried in fp32, keeps fp32 accuracy; the state itself stays in registers and
 // takes each chunk's U by one fp32 multiply-add per element.  S and M enter the
 // output's products as bf16 (half a step each, 2^-8 relative): y is rounded to
-// bf16 itself, and the three are of one size.
+// bf16 itself, and the three are of one size where the terms of a sum do not cancel;
+// where they do, y is off by half a step of their magnitudes.
 //
 // Roles (32 warps, one block per SM): wx (4 warps) weights x and stores its
 // terms; scores (8) turn G into M; state (16) holds S and combines YI, YM and
@@ -44,14 +45,15 @@
 //
 // Long sequences are cut into pieces that run in parallel (kda_ssm_pieces.cuh).
 //
-// Measured, 64K tokens, 96 heads, dk = 128, dv = 64 (48 tiles, three pieces): 0.91
-// ms on the same buffers again and again, of which 0.22 the first pass (0.95 us a
-// chunk) and 0.68 the second (2 us a chunk); 1.07 with other inputs in between.
-// The second pass is bound by the instructions around its products:
-// issue slots 64 % busy, the shared-memory pipe ~80 % (the roles' accesses and the
-// operands'), the tensor pipe 54 %, DRAM 31 %.  A state of 64 columns per thread
-// in eight warps (fewer instructions in all) does not fit the registers that
-// remain.
+// Measured, 64K tokens, 96 heads, dk = 128, dv = 64 (48 tiles, three pieces): 0.95
+// ms on the same buffers again and again, 1.10 with other inputs in between.  A
+// chunk takes 0.95 us in the first pass and 2 us in the second.  Nothing is
+// saturated in the second pass (issue slots 64 % busy, tensor pipe 52 %, the
+// shared-memory pipe of the roles' own accesses 42 %, DRAM 28 %): its time is what
+// the roles wait for one another along a chunk's chain of products.  U's four
+// terms are 60 % of the tensor work there and all of it in the first pass.  A state
+// of 64 columns per thread in eight warps (fewer instructions in all) does not fit
+// the registers that remain.
 #include <cuda.h>
 
 #include <algorithm>
